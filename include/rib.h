@@ -360,6 +360,148 @@ int rib_window_attn_bwd_masked(const void* qkv, const void* out, const void* dou
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The layer's other operators.
+ *
+ * A layer of the network around the attention is
+ *   x1 = x + W_o attn(W_qkv LN(x)),   y = x1 + FFN(LN(x1));
+ * the entry points below are its layer norms, its projections and its gated
+ * feed-forward block, forward and backward.  A feature map [B][H][W][C] is
+ * seen as `rows` = B*H*W rows of C channels; nothing here knows windows.
+ *
+ * Common to all of them: rows == 0 is a valid no-op (pointers not looked at)
+ * except that weight gradients, then empty sums, are zeroed; outputs must not
+ * overlap inputs unless an argument says so; sums over rows go through
+ * partials added in a fixed order, so repeated calls give the same bits.
+ * The products take bf16 operands with fp32 accumulation and every channel
+ * count a multiple of 8 (a 16-byte row pitch), at most 65536, else
+ * RIB_ERR_UNSUPPORTED; rows may be any number up to 2^30.
+ * ------------------------------------------------------------------------ */
+#define RIB_DTYPE_BF16 0
+#define RIB_DTYPE_F32  1
+
+/* Activations: none, gelu(z) = z Phi(z) (erf form), silu(z) = z / (1 + e^-z). */
+#define RIB_ACT_NONE 0
+#define RIB_ACT_GELU 1
+#define RIB_ACT_SILU 2
+
+/* ------------------------------------------------------------------------
+ * rib_layer_norm_fwd -- layer norm over the channels of each row:
+ *   mean = mean_c x,  rstd = 1 / sqrt(mean_c (x - mean)^2 + eps),
+ *   y = gamma (x - mean) rstd + beta.
+ *
+ *   x, y   : [rows][C], both of `dtype` (RIB_DTYPE_BF16 or RIB_DTYPE_F32);
+ *            y may be x
+ *   gamma, beta : fp32 [C]; NULL stands for ones / zeros
+ *   eps    : >= 0 (RIB_ERR_ARG otherwise)
+ *   mean, rstd : out, fp32 [rows], needed by the backward; may be NULL
+ * 1 <= C <= 8192 (any C; whole 16-byte vectors at 16-byte addresses are the
+ * fast case, other pointers need their element's alignment only).  All
+ * arithmetic is fp32; y is rounded once.
+ * ------------------------------------------------------------------------ */
+int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* gamma,
+                       const float* beta, float eps, void* y, float* mean, float* rstd,
+                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * rib_layer_norm_bwd -- its backward: with xh = (x - mean) rstd, g = gamma dy,
+ *   dx = rstd (g - mean_c g - xh mean_c (g xh)) + dres,
+ *   dgamma = sum_rows dy xh,  dbeta = sum_rows dy.
+ *
+ *   x, dy, dres, dx : [rows][C] of `dtype`; dres (a second gradient of x, as
+ *            the residual path's, added before the one rounding) may be NULL;
+ *            dx may be dy or dres
+ *   mean, rstd : from rib_layer_norm_fwd
+ *   gamma  : as given to the forward (NULL: ones)
+ *   dgamma, dbeta : out, fp32 [C]; either may be NULL (not wanted)
+ *   workspace : device, >= rib_layer_norm_bwd_workspace() bytes, 256-byte
+ *            aligned; not looked at when both sums are NULL
+ * ------------------------------------------------------------------------ */
+size_t rib_layer_norm_bwd_workspace(int rows, int C);
+int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C,
+                       const float* mean, const float* rstd, const float* gamma, const void* dres,
+                       void* dx, float* dgamma, float* dbeta, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rib_linear_fwd -- a projection with its epilogue:
+ *   z = x W^T + bias,   y = act(z) + residual.
+ *
+ *   x        : bf16 [rows][K]
+ *   w        : bf16 [N][K] (Linear layout [out][in])
+ *   bias     : fp32 [N] or NULL
+ *   act      : RIB_ACT_*
+ *   residual : bf16 [rows][N] or NULL
+ *   pre      : out, bf16 [rows][N], z for the backward, or NULL
+ *   y        : out, bf16 [rows][N]; may be residual
+ * z, act(z) and the sum are fp32; y and pre are each rounded once.
+ * ------------------------------------------------------------------------ */
+int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const float* bias,
+                   int act, const void* residual, void* pre, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rib_linear_bwd -- its backward (the residual's gradient is dy itself):
+ *   dz = dy act'(pre),  dx = dz W + dx_add,  dW = dz^T x,  db = sum_rows dz.
+ *
+ *   pre      : from rib_linear_fwd; looked at only when act is not
+ *              RIB_ACT_NONE
+ *   dy       : bf16 [rows][N]
+ *   dx_add   : bf16 [rows][K] or NULL, a second gradient of x
+ *   dx       : out, bf16 [rows][K], or NULL; may be dx_add
+ *   dw       : out, [N][K] of dw_dtype (RIB_DTYPE_*), or NULL
+ *   db       : out, fp32 [N], or NULL
+ *   workspace: device, >= rib_linear_bwd_workspace() bytes, 256-byte aligned
+ * Through an activation dz is rounded to bf16 for the two products (dW then
+ * carries that rounding, relative 2^-9 per term, whatever its type); db is
+ * summed from the fp32 dz.
+ * ------------------------------------------------------------------------ */
+size_t rib_linear_bwd_workspace(int rows, int K, int N, int act);
+int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act, const void* pre,
+                   const void* dy, const void* dx_add, void* dx, void* dw, int dw_dtype, float* db,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rib_gated_ffn_fwd -- gated feed-forward block:
+ *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u,
+ *   y = h Wo^T + b_out + residual.
+ *
+ *   x      : bf16 [rows][C]
+ *   w_in   : bf16 [2][hidden][C], Wg then Wu;  b_in : fp32 [2][hidden] or NULL
+ *   w_out  : bf16 [C][hidden];                 b_out : fp32 [C] or NULL
+ *   residual : bf16 [rows][C] or NULL
+ *   y      : out, bf16 [rows][C]; may be residual
+ *   workspace : device, >= rib_gated_ffn_fwd_workspace() bytes (h in bf16, as
+ *            the second product takes it), 256-byte aligned
+ * hidden <= 32768.
+ * ------------------------------------------------------------------------ */
+size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden);
+int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_in,
+                      const float* b_in, const void* w_out, const float* b_out, int act,
+                      const void* residual, void* y, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * rib_gated_ffn_bwd -- its backward, from x alone (g, u and h are computed
+ * again; the forward keeps nothing):
+ *   dh = dy Wo,  dg = dh u act'(g),  du = dh act(g),
+ *   dx = dg Wg + du Wu + dx_add,  dWg = dg^T x,  dWu = du^T x,  dWo = dy^T h,
+ *   dbg, dbu, dbo = sum_rows dg, du, dy.
+ *
+ *   dx     : out, bf16 [rows][C]; may be dx_add
+ *   dw_in  : out, [2][hidden][C];  dw_out : out, [C][hidden], of dw_dtype
+ *   db_in  : out, fp32 [2][hidden] or NULL;  db_out : out, fp32 [C] or NULL
+ *   workspace : device, >= rib_gated_ffn_bwd_workspace() bytes, 256-byte
+ *            aligned
+ * h, dg and du are rounded to bf16 for the products (dW carries that, whatever
+ * its type); db_in is summed from the fp32 dg, du.
+ * ------------------------------------------------------------------------ */
+size_t rib_gated_ffn_bwd_workspace(int rows, int C, int hidden);
+int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_in,
+                      const float* b_in, const void* w_out, int act, const void* dy,
+                      const void* dx_add, void* dx, void* dw_in, float* db_in, void* dw_out,
+                      float* db_out, int dw_dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
  * rib_window_gather / rib_window_scatter -- the window partition with cyclic
  * shift as a standalone copy (the same rolled TMA tile addressing the
  * attention kernels use), for bit-exact checks and for callers that want

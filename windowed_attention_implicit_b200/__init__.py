@@ -31,6 +31,10 @@ __all__ = [
     "rib_set_wait_limit_ns", "rib_set_bwd_kernel", "rib_bwd_kernel_for", "rib_debug_wait_timeout", "rib_version", "library",
     "rib_trace_enable", "rib_trace_collect", "rib_debug_exp2", "ClaGate", "rib_cla_gate",
     "rib_window_attn_fwd_cla", "rib_cla_bwd", "rib_cla_bwd_workspace",
+    "rib_layer_norm_fwd", "rib_layer_norm_bwd", "rib_layer_norm_bwd_workspace",
+    "rib_linear_fwd", "rib_linear_bwd", "rib_linear_bwd_workspace",
+    "GatedFfn", "rib_gated_ffn_fwd", "rib_gated_ffn_fwd_workspace",
+    "rib_gated_ffn_bwd", "rib_gated_ffn_bwd_workspace",
 ]
 
 
@@ -501,6 +505,291 @@ def rib_window_attn_bwd(qkv, out, dout, lse, window: int, shift: int, qp_bf16=No
         _ptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
         _stream(stream)), name)
     return {"dqkv": dqkv, "dqp": dqp, "dkp": dkp, "dmlp": dmlp}
+
+
+# ---------------------------------------------------------------- the layer's other operators
+
+_ACTS = {"none": _abi.RIB_ACT_NONE, "gelu": _abi.RIB_ACT_GELU, "silu": _abi.RIB_ACT_SILU}
+_DTYPES = {torch.bfloat16: _abi.RIB_DTYPE_BF16, torch.float32: _abi.RIB_DTYPE_F32}
+_MAX_ROWS = 1 << 30
+
+
+def _act(where: str, act: str) -> int:
+    if act not in _ACTS:
+        raise RibError(_abi.RIB_ERR_ARG, f"{where}: act {act!r} is none of {', '.join(_ACTS)}")
+    return _ACTS[act]
+
+
+def _dtype(where: str, name: str, dtype: torch.dtype) -> int:
+    if dtype not in _DTYPES:
+        raise RibError(_abi.RIB_ERR_UNSUPPORTED, f"{where}: {name} is {dtype}, not bfloat16 or float32")
+    return _DTYPES[dtype]
+
+
+def _rows(where: str, x: torch.Tensor, name: str = "x") -> Tuple[int, int]:
+    """x [..., C] seen as rows of C channels."""
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise RibError(_abi.RIB_ERR_ARG, f"{where}: {name} must be [..., channels]")
+    rows = x.numel() // x.shape[-1]
+    if rows > _MAX_ROWS:
+        raise RibError(_abi.RIB_ERR_UNSUPPORTED, f"{where}: {rows} rows, more than 2^30")
+    return rows, x.shape[-1]
+
+
+class _on:
+    """What a call allocates for itself (missing outputs, workspace) belongs to
+    the stream that the call runs on, also when that is not torch's current
+    one: memory of the current stream could still be in use by work queued
+    there, and could be handed out again while the call runs."""
+
+    def __init__(self, stream, device):
+        self.current = torch.cuda.current_stream(device) if device.type == "cuda" else None
+        self.side = None
+        if stream is not None and self.current is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.cuda_stream != self.current.cuda_stream:
+                self.side = stream
+
+    def empty(self, shape, device, dtype) -> torch.Tensor:
+        if self.side is None:
+            return torch.empty(shape, device=device, dtype=dtype)
+        with torch.cuda.stream(self.side):
+            return torch.empty(shape, device=device, dtype=dtype)
+
+    def output(self, given, shape, device, dtype) -> torch.Tensor:
+        """An output the caller will use on the current stream."""
+        if given is not None:
+            return given
+        t = self.empty(shape, device, dtype)
+        if self.side is not None:
+            t.record_stream(self.current)
+        return t
+
+    def workspace(self, given, need, device) -> torch.Tensor:
+        return self.empty(max(need, 256), device, torch.uint8) if given is None else given
+
+
+def rib_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                       beta: Optional[torch.Tensor] = None, eps: float = 1e-5, y=None, mean=None,
+                       rstd=None, stream=None):
+    """(y, mean, rstd): layer norm of x [..., C] (bf16 or fp32) over its last
+    axis, y like x, mean and rstd fp32 [...].  gamma, beta fp32 [C] or None."""
+    name = "rib_layer_norm_fwd"
+    rows, C = _rows(name, x)
+    dt, dev, on = _dtype(name, "x", x.dtype), x.device, _on(stream, x.device)
+    y = on.output(y, x.shape, dev, x.dtype)
+    mean = on.output(mean, x.shape[:-1], dev, torch.float32)
+    rstd = on.output(rstd, x.shape[:-1], dev, torch.float32)
+    _sizes(name, dev, y=(y, x.numel()), mean=(mean, rows), rstd=(rstd, rows), gamma=(gamma, C),
+           beta=(beta, C))
+    f32 = torch.float32
+    _check(library().rib_layer_norm_fwd(
+        _ptr(x, x.dtype, "x"), dt, rows, C, _ptr(gamma, f32, "gamma"), _ptr(beta, f32, "beta"),
+        float(eps), _ptr(y, x.dtype, "y"), _ptr(mean, f32, "mean"), _ptr(rstd, f32, "rstd"),
+        _stream(stream)), name)
+    return y, mean, rstd
+
+
+def rib_layer_norm_bwd_workspace(rows: int, C: int) -> int:
+    return int(library().rib_layer_norm_bwd_workspace(int(rows), int(C)))
+
+
+def rib_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       gamma: Optional[torch.Tensor] = None, dres: Optional[torch.Tensor] = None,
+                       dx=None, dgamma=None, dbeta=None, weight_grads: bool = True,
+                       workspace=None, stream=None):
+    """dict(dx, dgamma, dbeta) of rib_layer_norm_fwd.  dres: a second gradient
+    of x (the residual path's), added to dx before its rounding.  Without
+    weight_grads dgamma and dbeta are None."""
+    name = "rib_layer_norm_bwd"
+    rows, C = _rows(name, x)
+    dt, dev, on = _dtype(name, "x", x.dtype), x.device, _on(stream, x.device)
+    dx = on.output(dx, x.shape, dev, x.dtype)
+    if weight_grads:
+        dgamma = on.output(dgamma, (C,), dev, torch.float32)
+        dbeta = on.output(dbeta, (C,), dev, torch.float32)
+    else:
+        dgamma = dbeta = None
+    n = x.numel()
+    _sizes(name, dev, dy=(dy, n), mean=(mean, rows), rstd=(rstd, rows), gamma=(gamma, C),
+           dres=(dres, n), dx=(dx, n), dgamma=(dgamma, C), dbeta=(dbeta, C))
+    f32 = torch.float32
+    ptrs = [_ptr(x, x.dtype, "x"), _ptr(dy, x.dtype, "dy")]
+    workspace = on.workspace(workspace, rib_layer_norm_bwd_workspace(rows, C) if weight_grads else 0,
+                             dev)
+    _check(library().rib_layer_norm_bwd(
+        *ptrs, dt, rows, C, _ptr(mean, f32, "mean"), _ptr(rstd, f32, "rstd"),
+        _ptr(gamma, f32, "gamma"), _ptr(dres, x.dtype, "dres"), _ptr(dx, x.dtype, "dx"),
+        _ptr(dgamma, f32, "dgamma"), _ptr(dbeta, f32, "dbeta"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+    return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
+
+
+def _weight(where: str, w: torch.Tensor, K: int) -> int:
+    if w.dim() != 2 or w.shape[1] != K:
+        raise RibError(_abi.RIB_ERR_ARG, f"{where}: w must be [out][{K}], got {tuple(w.shape)}")
+    return w.shape[0]
+
+
+def rib_linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   act: str = "none", residual: Optional[torch.Tensor] = None,
+                   save_pre: bool = False, y=None, pre=None, stream=None):
+    """(y, pre): y = act(x w^T + bias) + residual for x bf16 [..., K], w bf16
+    [N][K], bias fp32 [N]; act "none", "gelu" (erf form) or "silu".  pre is
+    the bf16 x w^T + bias that the backward of an activation needs, when
+    save_pre (or a buffer for it) is given, else None."""
+    name, bf = "rib_linear_fwd", torch.bfloat16
+    rows, K = _rows(name, x)
+    N = _weight(name, w, K)
+    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    shape = (*x.shape[:-1], N)
+    y = on.output(y, shape, dev, bf)
+    pre = on.output(pre, shape, dev, bf) if save_pre or pre is not None else None
+    _sizes(name, dev, w=(w, N * K), bias=(bias, N), residual=(residual, rows * N), y=(y, rows * N),
+           pre=(pre, rows * N))
+    _check(library().rib_linear_fwd(
+        _ptr(x, bf, "x"), rows, K, _ptr(w, bf, "w"), N, _ptr(bias, torch.float32, "bias"), a,
+        _ptr(residual, bf, "residual"), _ptr(pre, bf, "pre"), _ptr(y, bf, "y"), _stream(stream)),
+        name)
+    return y, pre
+
+
+def rib_linear_bwd_workspace(rows: int, K: int, N: int, act: str = "none") -> int:
+    return int(library().rib_linear_bwd_workspace(int(rows), int(K), int(N),
+                                                  _act("rib_linear_bwd_workspace", act)))
+
+
+def rib_linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, act: str = "none",
+                   pre: Optional[torch.Tensor] = None, dx_add: Optional[torch.Tensor] = None,
+                   with_dx: bool = True, with_dw: bool = True, with_db: bool = True, dx=None,
+                   dw=None, db=None, dw_dtype: torch.dtype = torch.float32, workspace=None,
+                   stream=None):
+    """dict(dx, dw, db) of rib_linear_fwd for dy bf16 [..., N]; what is not
+    wanted (with_dx, with_dw, with_db) is None.  dx_add: a second gradient of x,
+    added to dx before its rounding.  dw is fp32 or bf16 (dw_dtype, or the type
+    of the buffer given)."""
+    name, bf = "rib_linear_bwd", torch.bfloat16
+    rows, K = _rows(name, x)
+    N = _weight(name, w, K)
+    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    if a != _abi.RIB_ACT_NONE and pre is None:
+        raise RibError(_abi.RIB_ERR_ARG, f"{name}: act {act!r} needs pre (rib_linear_fwd's, with save_pre)")
+    dx = on.output(dx, x.shape, dev, bf) if with_dx else None
+    dw = on.output(dw, (N, K), dev, dw_dtype) if with_dw else None
+    db = on.output(db, (N,), dev, torch.float32) if with_db else None
+    dt = _dtype(name, "dw", dw.dtype) if dw is not None else _abi.RIB_DTYPE_F32
+    _sizes(name, dev, w=(w, N * K), dy=(dy, rows * N), pre=(pre, rows * N), dx_add=(dx_add, rows * K),
+           dx=(dx, rows * K), dw=(dw, N * K), db=(db, N))
+    xp = _ptr(x, bf, "x")
+    workspace = on.workspace(workspace, rib_linear_bwd_workspace(rows, K, N, act), dev)
+    _check(library().rib_linear_bwd(
+        xp, rows, K, _ptr(w, bf, "w"), N, a, _ptr(pre, bf, "pre"), _ptr(dy, bf, "dy"),
+        _ptr(dx_add, bf, "dx_add"), _ptr(dx, bf, "dx"), _ptr(dw, None, "dw"), dt,
+        _ptr(db, torch.float32, "db"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+    return {"dx": dx, "dw": dw, "db": db}
+
+
+@dataclass
+class GatedFfn:
+    """Device weights of the gated feed-forward block: w_in bf16
+    [2][hidden][C] (the gate's projection, then the other), w_out bf16
+    [C][hidden]; biases fp32 [2][hidden] and [C], or None."""
+    w_in: torch.Tensor
+    b_in: Optional[torch.Tensor]
+    w_out: torch.Tensor
+    b_out: Optional[torch.Tensor]
+
+    @classmethod
+    def from_params(cls, w_in, b_in, w_out, b_out, device="cuda"):
+        def f(t, dtype):
+            return None if t is None else torch.as_tensor(t).detach().to(
+                device=device, dtype=dtype).contiguous()
+        return cls(f(w_in, torch.bfloat16), f(b_in, torch.float32), f(w_out, torch.bfloat16),
+                   f(b_out, torch.float32))
+
+    @property
+    def hidden(self) -> int:
+        return self.w_in.shape[1]
+
+
+def _ffn_sizes(where: str, ffn: GatedFfn, C: int):
+    if ffn.w_in.dim() != 3 or ffn.w_in.shape[0] != 2 or ffn.w_in.shape[2] != C:
+        raise RibError(_abi.RIB_ERR_ARG,
+                       f"{where}: w_in must be [2][hidden][{C}], got {tuple(ffn.w_in.shape)}")
+    H = ffn.hidden
+    if tuple(ffn.w_out.shape) != (C, H):
+        raise RibError(_abi.RIB_ERR_ARG,
+                       f"{where}: w_out must be [{C}][{H}], got {tuple(ffn.w_out.shape)}")
+    return H, {"w_in": (ffn.w_in, 2 * H * C), "b_in": (ffn.b_in, 2 * H), "w_out": (ffn.w_out, C * H),
+               "b_out": (ffn.b_out, C)}
+
+
+def rib_gated_ffn_fwd_workspace(rows: int, C: int, hidden: int) -> int:
+    return int(library().rib_gated_ffn_fwd_workspace(int(rows), int(C), int(hidden)))
+
+
+def rib_gated_ffn_fwd(x: torch.Tensor, ffn: GatedFfn, act: str = "silu",
+                      residual: Optional[torch.Tensor] = None, y=None, workspace=None,
+                      stream=None) -> torch.Tensor:
+    """y = (act(x Wg^T + bg) * (x Wu^T + bu)) Wo^T + b_out + residual for x
+    bf16 [..., C]."""
+    name, bf, f32 = "rib_gated_ffn_fwd", torch.bfloat16, torch.float32
+    rows, C = _rows(name, x)
+    H, sizes = _ffn_sizes(name, ffn, C)
+    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    y = on.output(y, x.shape, dev, bf)
+    _sizes(name, dev, residual=(residual, rows * C), y=(y, rows * C), **sizes)
+    xp = _ptr(x, bf, "x")
+    workspace = on.workspace(workspace, rib_gated_ffn_fwd_workspace(rows, C, H), dev)
+    _check(library().rib_gated_ffn_fwd(
+        xp, rows, C, H, _ptr(ffn.w_in, bf, "w_in"), _ptr(ffn.b_in, f32, "b_in"),
+        _ptr(ffn.w_out, bf, "w_out"), _ptr(ffn.b_out, f32, "b_out"), a,
+        _ptr(residual, bf, "residual"), _ptr(y, bf, "y"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+    return y
+
+
+def rib_gated_ffn_bwd_workspace(rows: int, C: int, hidden: int) -> int:
+    return int(library().rib_gated_ffn_bwd_workspace(int(rows), int(C), int(hidden)))
+
+
+def rib_gated_ffn_bwd(x: torch.Tensor, ffn: GatedFfn, dy: torch.Tensor, act: str = "silu",
+                      dx_add: Optional[torch.Tensor] = None, dx=None, dw_in=None, db_in=None,
+                      dw_out=None, db_out=None, dw_dtype: torch.dtype = torch.float32,
+                      workspace=None, stream=None):
+    """dict(dx, dw_in, db_in, dw_out, db_out) of rib_gated_ffn_fwd, from x and dy
+    alone (the residual's gradient is dy: pass it as dx_add where the
+    residual is x itself).  db_in and db_out are formed where the block has
+    that bias, else None; dw_in and dw_out are both fp32 or both bf16."""
+    name, bf, f32 = "rib_gated_ffn_bwd", torch.bfloat16, torch.float32
+    rows, C = _rows(name, x)
+    H, sizes = _ffn_sizes(name, ffn, C)
+    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    if dw_in is not None:
+        dw_dtype = dw_in.dtype
+    elif dw_out is not None:
+        dw_dtype = dw_out.dtype
+    dt = _dtype(name, "dw_in / dw_out", dw_dtype)
+    dx = on.output(dx, x.shape, dev, bf)
+    dw_in = on.output(dw_in, (2, H, C), dev, dw_dtype)
+    dw_out = on.output(dw_out, (C, H), dev, dw_dtype)
+    db_in = on.output(db_in, (2, H), dev, f32) if ffn.b_in is not None else None
+    db_out = on.output(db_out, (C,), dev, f32) if ffn.b_out is not None else None
+    _sizes(name, dev, dy=(dy, rows * C), dx_add=(dx_add, rows * C), dx=(dx, rows * C),
+           dw_in=(dw_in, 2 * H * C), dw_out=(dw_out, C * H), db_in=(db_in, 2 * H),
+           db_out=(db_out, C), **sizes)
+    xp = _ptr(x, bf, "x")
+    workspace = on.workspace(workspace, rib_gated_ffn_bwd_workspace(rows, C, H), dev)
+    _check(library().rib_gated_ffn_bwd(
+        xp, rows, C, H, _ptr(ffn.w_in, bf, "w_in"), _ptr(ffn.b_in, f32, "b_in"),
+        _ptr(ffn.w_out, bf, "w_out"), a, _ptr(dy, bf, "dy"), _ptr(dx_add, bf, "dx_add"),
+        _ptr(dx, bf, "dx"), _ptr(dw_in, dw_dtype, "dw_in"), _ptr(db_in, f32, "db_in"),
+        _ptr(dw_out, dw_dtype, "dw_out"), _ptr(db_out, f32, "db_out"), dt,
+        _ptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)), name)
+    return {"dx": dx, "dw_in": dw_in, "db_in": db_in, "dw_out": dw_out, "db_out": db_out}
 
 
 def rib_window_gather(x: torch.Tensor, window: int, shift: int, out=None, stream=None):

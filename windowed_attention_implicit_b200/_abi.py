@@ -20,6 +20,11 @@ RIB_ERR_TIMEOUT = -6
 RIB_ERR_ALIGN = -7
 RIB_ERR_BOUNDS = -8
 RIB_NOALLOC_SCRATCH_BYTES = 24 * 1024 * 1024
+RIB_DTYPE_BF16 = 0
+RIB_DTYPE_F32 = 1
+RIB_ACT_NONE = 0
+RIB_ACT_GELU = 1
+RIB_ACT_SILU = 2
 RIB_BWD_AUTO = 0
 RIB_BWD_PER_ITEM = 1
 RIB_BWD_PERSISTENT = 2
@@ -79,6 +84,20 @@ _SIGS = {
                                         ctypes.POINTER(rib_mlp_t),
                                         ctypes.POINTER(rib_mlp_grad_t), _p, ctypes.c_size_t,
                                         _p]),
+    "rib_layer_norm_fwd": (_i, [_p, _i, _i, _i, _p, _p, ctypes.c_float, _p, _p, _p, _p]),
+    "rib_layer_norm_bwd_workspace": (ctypes.c_size_t, [_i, _i]),
+    "rib_layer_norm_bwd": (_i, [_p, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p,
+                                ctypes.c_size_t, _p]),
+    "rib_linear_fwd": (_i, [_p, _i, _i, _p, _i, _p, _i, _p, _p, _p, _p]),
+    "rib_linear_bwd_workspace": (ctypes.c_size_t, [_i, _i, _i, _i]),
+    "rib_linear_bwd": (_i, [_p, _i, _i, _p, _i, _i, _p, _p, _p, _p, _p, _i, _p, _p,
+                            ctypes.c_size_t, _p]),
+    "rib_gated_ffn_fwd_workspace": (ctypes.c_size_t, [_i, _i, _i]),
+    "rib_gated_ffn_fwd": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _i, _p, _p, _p,
+                               ctypes.c_size_t, _p]),
+    "rib_gated_ffn_bwd_workspace": (ctypes.c_size_t, [_i, _i, _i]),
+    "rib_gated_ffn_bwd": (_i, [_p, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _p, _i,
+                               _p, ctypes.c_size_t, _p]),
     "rib_window_gather": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "rib_window_scatter": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "rib_status_string": (ctypes.c_char_p, [_i]),

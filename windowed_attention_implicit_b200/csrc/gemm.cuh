@@ -1,0 +1,704 @@
+// gemm.cuh -- matrix products of the layer's projections on tcgen05 tensor
+// cores, bf16 operands and fp32 accumulation, with the work around each
+// product in its epilogue.
+//
+//   kLinear   z = x W^T + b,  y = act(z) + residual   (x [M][K], W [N][K])
+//   kDx       y = x W + residual                       (x [M][K], W [K][N])
+//   kGated    y = act(x Wg^T + bg) (x Wu^T + bu)       (W [2][N][K])
+//   dw_kernel dW = dz^T x, db = sum_rows dz            (dz [R][N], x [R][K])
+//
+// gemm_kernel is persistent and warp-specialised: warp 8 feeds a ring of
+// 64-deep operand tiles by TMA, warp 9 issues the MMAs of 128 x bn tiles
+// into one of two accumulators in tensor memory, warps 0-7 are the epilogue
+// of the other one.  Operand tiles are rows of 128 bytes in the 128-byte
+// swizzle, the layout the tensor core reads without bank conflicts; rows and
+// channels outside the matrices are the TMA's zero fill, and outputs outside
+// are clipped by the TMA store, so any M and any N, K that are multiples of
+// 8 (a 16-byte row pitch) run without a special case.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace rib {
+
+constexpr int SITE_GEMM = 50, SITE_DW = 51, SITE_FFN = 52;
+constexpr int G_GEMM_RES = 170, G_GEMM_BIAS = 171, G_DW_PART = 172, G_DW_RED = 173,
+              G_DZ_IN = 174, G_DZ_OUT = 175, G_FFN_PART = 176;
+
+enum GemmMode { kLinear = 0, kDx = 1, kGated = 2 };
+enum ActKind { kActNone = 0, kActGelu = 1, kActSilu = 2 };
+
+// ---------------------------------------------------------------- 2-D / 3-D TMA
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- activations
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// gelu(z) = z Phi(z), Phi the normal distribution function.  With t = |z| /
+// sqrt 2 and k = 1 / (1 + p t), Abramowitz and Stegun's formula 7.1.26 gives
+// erfc(t) = (a1 k + ... + a5 k^5) e^(-t^2) to 1.5e-7, so with Q = erfc(t) / 2
+// the value is max(z, 0) - |z| Q without a branch on the sign, and the slope
+// Phi + z phi takes the same exponential.  (|z| is capped in its product
+// with Q, whose value there is 0, so that an infinite z gives no NaN.)
+struct GeluParts {
+  float q, e;   // erfc(|z| / sqrt 2) / 2, exp(-z^2 / 2)
+};
+__device__ __forceinline__ GeluParts gelu_parts(float z) {
+  const float az = fabsf(z);
+  const float k = rcp_approx(fmaf(az, 0.3275911f * 0.70710678f, 1.f));
+  GeluParts r;
+  r.e = ex2_approx(z * z * (-0.5f * kLog2e));
+  float p = fmaf(k, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  p = fmaf(p, k, 0.5f * 1.421413741f);
+  p = fmaf(p, k, 0.5f * -0.284496736f);
+  p = fmaf(p, k, 0.5f * 0.254829592f);
+  r.q = p * k * r.e;
+  return r;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == kActGelu) {
+    const GeluParts g = gelu_parts(z);
+    return fmaf(-fminf(fabsf(z), 1e4f), g.q, fmaxf(z, 0.f));
+  } else if constexpr (ACT == kActSilu) {
+    return z * rcp_approx(1.f + ex2_approx(-kLog2e * z));
+  } else {
+    return z;
+  }
+}
+
+// act(z) and act'(z)
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& a, float& da) {
+  if constexpr (ACT == kActGelu) {
+    const GeluParts g = gelu_parts(z);
+    const float cap = fminf(fmaxf(z, -1e4f), 1e4f);
+    a = fmaf(-fabsf(cap), g.q, fmaxf(z, 0.f));
+    da = fmaf(cap, 0.3989422804f * g.e, z > 0.f ? 1.f - g.q : g.q);
+  } else if constexpr (ACT == kActSilu) {
+    const float s = rcp_approx(1.f + ex2_approx(-kLog2e * z));
+    a = z * s;
+    da = fmaf(a, 1.f - s, s);
+  } else {
+    a = z;
+    da = 1.f;
+  }
+}
+
+// ---------------------------------------------------------------- the product
+constexpr int kGemmThreads = 320;
+constexpr uint32_t kGemmATile = 128u * 128u;        // 128 rows x 64 channels
+constexpr uint32_t kGemmStage = 32u * 128u;         // one warp's staging: 32 rows x 64 columns
+constexpr uint32_t kGemmStaging = 8u * kGemmStage;
+constexpr int kGemmMaxStages = 10;
+
+struct GemmParams {
+  const float* bias;               // [N], or [2][N] for kGated; may be null
+  const __nv_bfloat16* residual;   // [M][N]; may be null
+  int has_pre;                     // z is stored through tm_pre
+  int M, N, K;
+  int bn;                          // columns of a B tile in shared memory (64 .. 256)
+  int m_tiles, n_tiles;
+  int splits;                      // the row tiles of one column tile go to `splits` items
+  int k_steps, stages;
+  int b_resident;                  // the column tile's weights stay in shared memory
+  uint64_t wait_limit_ns;
+};
+
+struct GemmBars {
+  uint64_t full[kGemmMaxStages], empty[kGemmMaxStages];
+  uint64_t acc_full[2], acc_free[2], b_full, b_free, drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__host__ __device__ __forceinline__ size_t gemm_smem_bytes(int bn, int stages, int k_steps,
+                                                           bool resident) {
+  const size_t b = static_cast<size_t>(bn) * 128;
+  return 1024 + stages * (kGemmATile + (resident ? 0 : b)) + (resident ? k_steps * b : 0) +
+         kGemmStaging + sizeof(GemmBars);
+}
+
+// Columns of y that one tile gives: half of the B tile for kGated (the other
+// half is the second projection's).
+template <int MODE>
+__device__ __forceinline__ int gemm_tile_cols(const GemmParams& p) {
+  return MODE == kGated ? p.bn / 2 : p.bn;
+}
+
+// Loads the B tile of column tile n, k-step k (64 deep) to `dst`.
+template <int MODE>
+__device__ __forceinline__ void gemm_load_b(uint8_t* dst, const CUtensorMap* tm_b, uint64_t* bar,
+                                            const GemmParams& p, int n0, int k) {
+  if constexpr (MODE == kLinear) {
+    tma_load_2d(dst, tm_b, bar, 64 * k, n0);
+  } else if constexpr (MODE == kGated) {
+    tma_load_2d(dst, tm_b, bar, 64 * k, n0);
+    tma_load_2d(dst + p.bn * 64, tm_b, bar, 64 * k, p.N + n0);
+  } else {
+    for (int c = 0; c < p.bn / 64; ++c) tma_load_2d(dst + c * 8192, tm_b, bar, n0 + 64 * c, 64 * k);
+  }
+}
+
+// Work item i: column tile i % n_tiles, row tiles i / n_tiles + splits * j.
+// Items that run at the same time so share their x rows (one read from HBM
+// serves all column tiles), and a CTA keeps its column tile's weights.
+// grid min(items, SMs), block kGemmThreads, dynamic smem gemm_smem_bytes().
+template <int MODE, int ACT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_y,
+                const __grid_constant__ CUtensorMap tm_pre, const GemmParams p) {
+  extern __shared__ uint8_t gemm_raw[];
+  uint8_t* base = gemm_raw + ((1024u - (smem_u32(gemm_raw) & 1023u)) & 1023u);
+  const uint32_t b_bytes = static_cast<uint32_t>(p.bn) * 128u;
+  const uint32_t stage_bytes = kGemmATile + (p.b_resident ? 0u : b_bytes);
+  uint8_t* s_res = base + p.stages * stage_bytes;
+  uint8_t* s_stage = s_res + (p.b_resident ? p.k_steps * b_bytes : 0u);
+  GemmBars& bb = *reinterpret_cast<GemmBars*>(s_stage + kGemmStaging);
+  volatile int* ab = &bb.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tn = gemm_tile_cols<MODE>(p);
+  const int items = p.n_tiles * p.splits;
+  const uint64_t lim = p.wait_limit_ns;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&bb.full[i], 1);
+      mbar_init(&bb.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bb.acc_full[i], 1);
+      mbar_init(&bb.acc_free[i], 8);
+    }
+    mbar_init(&bb.b_full, 1);
+    mbar_init(&bb.b_free, 1);
+    mbar_init(&bb.drain, 1);
+    bb.abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_y);
+  }
+  if (warp == 9) {
+    tmem_alloc(&bb.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem;
+
+  if (warp == 8) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int q = 0, st = 0, n_item = 0;   // running load number, its stage
+      uint32_t ph = 1;                 // parity of the previous use of the stage
+      for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
+        const int n0 = (it % p.n_tiles) * tn;
+        if (p.b_resident) {
+          if (n_item > 0 && !(ok = mbar_wait(&bb.b_free, (n_item - 1) & 1, ab, lim, SITE_GEMM)))
+            break;
+          mbar_arrive_expect_tx(&bb.b_full, p.k_steps * b_bytes);
+          for (int k = 0; k < p.k_steps; ++k)
+            gemm_load_b<MODE>(s_res + k * b_bytes, &tm_b, &bb.b_full, p, n0, k);
+        }
+        for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits)
+          for (int k = 0; k < p.k_steps; ++k) {
+            if (q >= p.stages && !(ok = mbar_wait(&bb.empty[st], ph, ab, lim, SITE_GEMM))) break;
+            uint8_t* sa = base + st * stage_bytes;
+            mbar_arrive_expect_tx(&bb.full[st], stage_bytes);
+            tma_load_2d(sa, &tm_a, &bb.full[st], 64 * k, 128 * m);
+            if (!p.b_resident) gemm_load_b<MODE>(sa + kGemmATile, &tm_b, &bb.full[st], p, n0, k);
+            ++q;
+            if (++st == p.stages) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+      }
+      if (*ab) {
+        // loads still in flight land before the CTA exits
+        volatile int no_abort = 0;
+        if (p.b_resident && n_item > 0)
+          mbar_wait(&bb.b_full, (n_item - 1) & 1, &no_abort, 200000000ull, SITE_GEMM);
+        for (int i = max(0, q - p.stages); i < q; ++i)
+          mbar_wait(&bb.full[i % p.stages], (i / p.stages) & 1, &no_abort, 200000000ull, SITE_GEMM);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- MMA issue
+    const int last_steps = (p.K - 64 * (p.k_steps - 1) + 15) / 16;
+    bool ok = true;
+    int st = 0, t = 0, n_item = 0;
+    uint32_t ph = 0;
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
+      const int n0 = (it % p.n_tiles) * tn;
+      // a last column tile narrower than bn takes a narrower MMA
+      const int cols = MODE == kGated ? p.bn : min(p.bn, ((p.N - n0 + 15) >> 4) << 4);
+      const uint32_t idesc = make_idesc_bf16(128, cols, false, MODE == kDx);
+      if (p.b_resident && !(ok = warp_wait(&bb.b_full, n_item & 1, ab, lim, SITE_GEMM))) break;
+      for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
+        const int a = t & 1;
+        if (t >= 2 && !(ok = warp_wait(&bb.acc_free[a], ((t >> 1) - 1) & 1, ab, lim, SITE_GEMM)))
+          break;
+        for (int k = 0; k < p.k_steps; ++k) {
+          if (!(ok = warp_wait(&bb.full[st], ph, ab, lim, SITE_GEMM))) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(base + st * stage_bytes);
+          const uint32_t sb = p.b_resident ? smem_u32(s_res + k * b_bytes) : sa + kGemmATile;
+          // K-major: a K = 16 step is 32 bytes along the rows; MN-major
+          // (kDx): it is 16 rows of 128 bytes, 64-column chunks 8 KB apart
+          const uint64_t ad = make_sdesc(sa, 16, 1024, kLayoutSW128);
+          const uint64_t bd = MODE == kDx ? make_sdesc(sb, 8192, 1024, kLayoutSW128)
+                                          : make_sdesc(sb, 16, 1024, kLayoutSW128);
+          const int steps = k + 1 == p.k_steps ? last_steps : 4;
+          for (int s = 0; s < steps; ++s)
+            umma_ss_elect(tmem + 256 * a, ad + 2 * s, bd + (MODE == kDx ? 128 : 2) * s, idesc,
+                          (k > 0 || s > 0) ? 1u : 0u);
+          umma_commit_elect(&bb.empty[st]);
+          if (++st == p.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit_elect(&bb.acc_full[a]);
+      }
+      if (ok && p.b_resident) umma_commit_elect(&bb.b_free);
+    }
+    // every MMA issued above completes before the tensor memory is freed
+    umma_commit_elect(&bb.drain);
+    volatile int no_abort = 0;
+    mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_GEMM);
+  } else {
+    // ---------------------------------------------------------- epilogue
+    // warp w: TMEM lane quarter w % 4 (tile rows 32 (w % 4) ..), every other
+    // 64-column chunk from w / 4.  A chunk goes through the warp's own 4 KB
+    // of shared memory (rows of 128 bytes, 128-byte swizzle) to one TMA store.
+    const int quarter = warp & 3, half = warp >> 2;
+    uint8_t* sg = s_stage + warp * kGemmStage;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const size_t res_n = static_cast<size_t>(p.M) * p.N;
+    int t = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      const int n0 = (it % p.n_tiles) * tn;
+      const int cols = min(tn, p.N - n0), chunks = (cols + 63) / 64;
+      for (int m = it / p.n_tiles; m < p.m_tiles; m += p.splits, ++t) {
+        const int a = t & 1;
+        const int row0 = 128 * m + 32 * quarter;
+        const bool row_in = row0 + lane < p.M;
+        if (!(ok = warp_wait(&bb.acc_full[a], (t >> 1) & 1, ab, lim, SITE_GEMM))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + 256 * a + lane_off;
+        for (int c = half; c < chunks; c += 2) {
+          uint32_t out[32], pre[MODE == kLinear ? 32 : 1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = n0 + 64 * c + 32 * h;   // first of 32 columns
+            uint4 res[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const size_t at = static_cast<size_t>(row0 + lane) * p.N + col + 8 * e;
+              res[e] = (MODE != kGated && p.residual && row_in && col + 8 * e < p.N &&
+                        rib_guard(at + 7, res_n, G_GEMM_RES))
+                           ? __ldg(reinterpret_cast<const uint4*>(p.residual + at))
+                           : make_uint4(0, 0, 0, 0);
+            }
+            uint32_t v[32];
+            tmem_ld_x32(acc + 64 * c + 32 * h, v);
+            if constexpr (MODE == kGated) {
+              uint32_t u[32];
+              tmem_ld_x32(acc + tn + 64 * c + 32 * h, u);
+              tmem_wait_ld();
+              reg_fence_x32(v);
+              reg_fence_x32(u);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4 bg = make_float4(0.f, 0.f, 0.f, 0.f), bu = bg;
+                if (p.bias && col + 4 * e < p.N &&
+                    rib_guard(static_cast<size_t>(p.N) + col + 4 * e + 3, 2ull * p.N, G_GEMM_BIAS)) {
+                  bg = __ldg(reinterpret_cast<const float4*>(p.bias + col + 4 * e));
+                  bu = __ldg(reinterpret_cast<const float4*>(p.bias + p.N + col + 4 * e));
+                }
+                const float b4[4] = {bg.x, bg.y, bg.z, bg.w}, c4[4] = {bu.x, bu.y, bu.z, bu.w};
+                float y4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y4[i] = act_value<ACT>(__uint_as_float(v[4 * e + i]) + b4[i]) *
+                          (__uint_as_float(u[4 * e + i]) + c4[i]);
+                out[16 * h + 2 * e] = pack_bf16x2(y4[0], y4[1]);
+                out[16 * h + 2 * e + 1] = pack_bf16x2(y4[2], y4[3]);
+              }
+            } else {
+              tmem_wait_ld();
+              reg_fence_x32(v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (MODE == kLinear && p.bias && col + 4 * e < p.N &&
+                    rib_guard(static_cast<size_t>(col) + 4 * e + 3, static_cast<size_t>(p.N),
+                              G_GEMM_BIAS))
+                  bv = __ldg(reinterpret_cast<const float4*>(p.bias + col + 4 * e));
+                const float z0 = __uint_as_float(v[4 * e]) + bv.x;
+                const float z1 = __uint_as_float(v[4 * e + 1]) + bv.y;
+                const float z2 = __uint_as_float(v[4 * e + 2]) + bv.z;
+                const float z3 = __uint_as_float(v[4 * e + 3]) + bv.w;
+                const uint32_t r01 = e & 1 ? res[e >> 1].z : res[e >> 1].x;
+                const uint32_t r23 = e & 1 ? res[e >> 1].w : res[e >> 1].y;
+                if constexpr (MODE == kLinear) {
+                  pre[16 * h + 2 * e] = pack_bf16x2(z0, z1);
+                  pre[16 * h + 2 * e + 1] = pack_bf16x2(z2, z3);
+                }
+                out[16 * h + 2 * e] =
+                    pack_bf16x2(act_value<ACT>(z0) + __uint_as_float(r01 << 16),
+                                act_value<ACT>(z1) + __uint_as_float(r01 & 0xffff0000u));
+                out[16 * h + 2 * e + 1] =
+                    pack_bf16x2(act_value<ACT>(z2) + __uint_as_float(r23 << 16),
+                                act_value<ACT>(z3) + __uint_as_float(r23 & 0xffff0000u));
+              }
+            }
+          }
+          if (c + 2 >= chunks) {   // this warp has read its last columns
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bb.acc_free[a]);
+          }
+          auto put = [&](const uint32_t* w, const CUtensorMap* map) {
+            if (lane == 0) tma_store_wait_read_all();   // the last store has read the buffer
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              *reinterpret_cast<uint4*>(sg + lane * 128 + ((g ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(map, sg, n0 + 64 * c, row0);
+              tma_store_commit();
+            }
+          };
+          if (row0 < p.M) {
+            if constexpr (MODE == kLinear) {
+              if (p.has_pre) put(pre, &tm_pre);
+            }
+            put(out, &tm_y);
+          }
+        }
+        if (half >= chunks) {   // no columns for this warp in a narrow tile
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bb.acc_free[a]);
+        }
+      }
+    }
+    // the stores are complete before the kernel's work is considered done
+    if (lane == 0) tma_store_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- dW, db
+// dW[n][k] = sum_r dz[r][n] x[r][k] and db[n] = sum_r dz[r][n]: the rows are
+// the contraction, so both operands are MN-major (64 rows of 64 channels are
+// one canonical 8 KB atom column).  A CTA takes a tile of 256 x 192 of dW (two
+// accumulators of 128 rows) and a range of the rows; the ranges' partial
+// sums go to the workspace and dw_reduce_kernel adds them in order.  db is
+// one more column of the product: a block of ones stands behind x's channels
+// in each stage, so the sum of the bf16 dz is exact up to fp32 accumulation
+// and costs 16 of 208 MMA columns and no pass over dz.
+constexpr int kDwStages = 3;
+constexpr int kDwBn = 192;
+constexpr uint32_t kDwAtom = 8192;                       // 64 rows x 64 channels
+constexpr uint32_t kDwStageBytes = (4 + 4) * kDwAtom;    // dz: 4 atoms; x: 3, ones: 1
+
+struct DwParams {
+  int rows, N, K;
+  int m_tiles, n_tiles, splits;
+  int steps, steps_per_split;      // 64-row steps, in all and per split
+  float* part;                     // [splits][N][K]
+  float* part_db;                  // [splits][N]; null: no db
+  uint64_t wait_limit_ns;
+};
+
+struct DwBars {
+  uint64_t full[kDwStages], empty[kDwStages], acc_full, drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__host__ __device__ __forceinline__ size_t dw_smem_bytes() {
+  return 1024 + kDwStages * kDwStageBytes + sizeof(DwBars);
+}
+
+// grid m_tiles * n_tiles * splits, block kGemmThreads, dynamic smem dw_smem_bytes().
+// tm_z: dz [rows][N], tm_x: x [rows][K], boxes of 64 channels x 64 rows,
+// 128-byte swizzle.
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    dw_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_x,
+              const DwParams p) {
+  extern __shared__ uint8_t dwg_raw[];
+  uint8_t* base = dwg_raw + ((1024u - (smem_u32(dwg_raw) & 1023u)) & 1023u);
+  DwBars& bb = *reinterpret_cast<DwBars*>(base + kDwStages * kDwStageBytes);
+  volatile int* ab = &bb.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = p.m_tiles * p.n_tiles;
+  const int tile = blockIdx.x % tiles, split = blockIdx.x / tiles;
+  const int m0 = (tile / p.n_tiles) * 256, k0 = (tile % p.n_tiles) * kDwBn;
+  const int a_chunks = min(4, (p.N - m0 + 63) / 64), b_chunks = min(3, (p.K - k0 + 63) / 64);
+  const int blocks = p.N - m0 > 128 ? 2 : 1;
+  const bool with_db = p.part_db != nullptr && k0 == 0;
+  const int s0 = split * p.steps_per_split, s1 = min(p.steps, s0 + p.steps_per_split);
+  const uint64_t lim = p.wait_limit_ns;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDwStages; ++i) {
+      mbar_init(&bb.full[i], 1);
+      mbar_init(&bb.empty[i], 1);
+    }
+    mbar_init(&bb.acc_full, 1);
+    mbar_init(&bb.drain, 1);
+    bb.abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (with_db) {
+    // ones behind x's atoms (every element: the swizzle does not matter)
+    for (int i = threadIdx.x; i < kDwStages * 512; i += kGemmThreads)
+      *reinterpret_cast<uint4*>(base + (i / 512) * kDwStageBytes + (4 + b_chunks) * kDwAtom +
+                                (i % 512) * 16) =
+          make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bb.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem;
+  bool ok = true;
+  if (warp == 8) {
+    if (lane == 0) {
+      int q = 0;
+      for (int s = s0; ok && s < s1; ++s, ++q) {
+        const int st = q % kDwStages;
+        if (q >= kDwStages &&
+            !(ok = mbar_wait(&bb.empty[st], (q / kDwStages - 1) & 1, ab, lim, SITE_DW)))
+          break;
+        uint8_t* sa = base + st * kDwStageBytes;
+        mbar_arrive_expect_tx(&bb.full[st], (a_chunks + b_chunks) * kDwAtom);
+        for (int c = 0; c < a_chunks; ++c)
+          tma_load_2d(sa + c * kDwAtom, &tm_z, &bb.full[st], m0 + 64 * c, 64 * s);
+        for (int c = 0; c < b_chunks; ++c)
+          tma_load_2d(sa + (4 + c) * kDwAtom, &tm_x, &bb.full[st], k0 + 64 * c, 64 * s);
+      }
+      if (*ab) {
+        volatile int no_abort = 0;
+        for (int i = max(0, q - kDwStages); i < q; ++i)
+          mbar_wait(&bb.full[i % kDwStages], (i / kDwStages) & 1, &no_abort, 200000000ull, SITE_DW);
+      }
+    }
+  } else if (warp == 9) {
+    const uint32_t idesc = make_idesc_bf16(128, 64 * b_chunks + (with_db ? 16 : 0), true, true);
+    int q = 0;
+    for (int s = s0; ok && s < s1; ++s, ++q) {
+      const int st = q % kDwStages;
+      if (!(ok = warp_wait(&bb.full[st], (q / kDwStages) & 1, ab, lim, SITE_DW))) break;
+      tc_fence_after();
+      const uint32_t sa = smem_u32(base + st * kDwStageBytes);
+      const uint64_t bd = make_sdesc(sa + 4 * kDwAtom, kDwAtom, 1024, kLayoutSW128);
+      for (int b = 0; b < blocks; ++b) {
+        const uint64_t ad = make_sdesc(sa + 2 * b * kDwAtom, kDwAtom, 1024, kLayoutSW128);
+        for (int k = 0; k < 4; ++k)
+          umma_ss_elect(tmem + 256 * b, ad + 128 * k, bd + 128 * k, idesc,
+                        (q > 0 || k > 0) ? 1u : 0u);
+      }
+      umma_commit_elect(&bb.empty[st]);
+    }
+    if (ok) umma_commit_elect(&bb.acc_full);
+    umma_commit_elect(&bb.drain);
+    volatile int no_abort = 0;
+    mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_DW);
+  } else if ((warp >> 2) < blocks) {
+    // warp w: rows 32 (w % 4) .. of block w / 4, every column
+    ok = warp_wait(&bb.acc_full, 0, ab, lim, SITE_DW);
+    tc_fence_after();
+    const int blk = warp >> 2;
+    const int n = m0 + 128 * blk + 32 * (warp & 3) + lane;
+    const uint32_t acc = tmem + 256 * blk + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const size_t row = static_cast<size_t>(split) * p.N + n;
+    const size_t part_n = static_cast<size_t>(p.splits) * p.N * p.K;
+    if (ok) {
+      for (int c = 0; c < 2 * b_chunks; ++c) {
+        uint32_t v[32];
+        tmem_ld_x32(acc + 32 * c, v);
+        tmem_wait_ld();
+        reg_fence_x32(v);
+        const int k = k0 + 32 * c;
+        if (n < p.N) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const size_t at = row * p.K + k + 4 * e;
+            if (k + 4 * e < p.K && rib_guard(at + 3, part_n, G_DW_PART))
+              *reinterpret_cast<float4*>(p.part + at) =
+                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                              __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+          }
+        }
+      }
+      if (with_db) {
+        uint32_t v[16];
+        tmem_ld_x16(acc + 64 * b_chunks, v);
+        tmem_wait_ld();
+        reg_fence_x16(v);
+        if (n < p.N && rib_guard(row, static_cast<size_t>(p.splits) * p.N, G_DW_PART))
+          p.part_db[row] = __uint_as_float(v[0]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dW = sum of the splits' partials, in order; fp32 or rounded to bf16 once.
+// n = N * K (a multiple of 4); grid ceil(n / 4 / 256), block 256.
+__global__ void __launch_bounds__(256)
+    dw_reduce_kernel(const float* part, int splits, size_t n, float* out32, __nv_bfloat16* out16) {
+  const size_t i = 4 * (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x);
+  if (i >= n) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) {
+    const size_t at = static_cast<size_t>(k) * n + i;
+    if (!rib_guard(at + 3, static_cast<size_t>(splits) * n, G_DW_RED)) continue;
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part + at));
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  if (out32) {
+    *reinterpret_cast<float4*>(out32 + i) = s;
+  } else {
+    *reinterpret_cast<uint2*>(out16 + i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
+
+// ---------------------------------------------------------------- dz
+// dz = dy act'(pre), rounded to bf16 for the products that follow (their
+// operands are bf16), and per-row-range column sums of the unrounded fp32
+// dz.  A thread keeps one channel octet over its rows.  With pre null dz is
+// dy itself and only the sums are formed.
+// grid (ceil(N / 256), row splits), block 256: 32 octets x 8 row slots.
+struct DzParams {
+  const __nv_bfloat16* dy;
+  const __nv_bfloat16* pre;   // null: act none, sums only
+  __nv_bfloat16* dz;
+  float* part;                // [gridDim.y][N]; null: no sums
+  int rows, N;
+};
+
+template <int ACT>
+__global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
+  __shared__ float sums[8][256];
+  const int oct = threadIdx.x & 31, slot = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + 8 * oct;
+  const size_t n = static_cast<size_t>(p.rows) * p.N;
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  const bool in = c < p.N;
+  constexpr int B = 4;   // rows in flight per thread
+  const long long step = 8ll * gridDim.y;
+  for (long long r0 = slot + 8ll * blockIdx.y; in && r0 < p.rows; r0 += B * step) {
+    uint4 dv[B], zv[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const long long r = r0 + k * step;
+      const size_t at = static_cast<size_t>(r) * p.N + c;
+      const bool ok = r < p.rows && rib_guard(at + 7, n, G_DZ_IN);
+      dv[k] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + at)) : make_uint4(0, 0, 0, 0);
+      zv[k] = ok && ACT != kActNone ? __ldg(reinterpret_cast<const uint4*>(p.pre + at))
+                                    : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const long long r = r0 + k * step;
+      if (r >= p.rows) break;
+      const uint32_t dw[4] = {dv[k].x, dv[k].y, dv[k].z, dv[k].w};
+      const uint32_t zw[4] = {zv[k].x, zv[k].y, zv[k].z, zv[k].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float d0 = __uint_as_float(dw[e] << 16), d1 = __uint_as_float(dw[e] & 0xffff0000u);
+        if constexpr (ACT != kActNone) {
+          float a, g0, g1;
+          act_both<ACT>(__uint_as_float(zw[e] << 16), a, g0);
+          act_both<ACT>(__uint_as_float(zw[e] & 0xffff0000u), a, g1);
+          d0 *= g0;
+          d1 *= g1;
+          o[e] = pack_bf16x2(d0, d1);
+        }
+        acc[2 * e] += d0;
+        acc[2 * e + 1] += d1;
+      }
+      if constexpr (ACT != kActNone) {
+        const size_t at = static_cast<size_t>(r) * p.N + c;
+        if (rib_guard(at + 7, n, G_DZ_OUT))
+          *reinterpret_cast<uint4*>(p.dz + at) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[slot][8 * oct + e] = acc[e];
+  __syncthreads();
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < p.N) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += sums[k][threadIdx.x];
+    const size_t at = static_cast<size_t>(blockIdx.y) * p.N + col;
+    if (rib_guard(at, static_cast<size_t>(gridDim.y) * p.N, G_DW_PART)) p.part[at] = s;
+  }
+}
+
+}  // namespace rib

@@ -1,0 +1,644 @@
+// layer_api.cuh -- entry points of the layer's other operators: layer norm,
+// linear projections, the gated feed-forward block (include/rib.h).  Host
+// side only: validation, launch shapes, tensor maps, workspace carving.
+// Included once, at the end of rib.cu, whose helpers it uses.
+#pragma once
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "layer_norm.cuh"
+#include "gemm.cuh"
+#include "ffn.cuh"
+
+namespace rib {
+namespace {
+
+// ---------------------------------------------------------------- shapes
+
+constexpr int kMaxChannels = 65536;
+constexpr int kMaxRows = 1 << 30;
+constexpr size_t kSmemMax = 227 * 1024;
+
+int check_product(int rows, int K, int N) {
+  if (rows < 0 || K <= 0 || N <= 0) return RIB_ERR_ARG;
+  if (K % 8 || N % 8 || K > kMaxChannels || N > kMaxChannels || rows > kMaxRows)
+    return RIB_ERR_UNSUPPORTED;
+  return RIB_OK;
+}
+
+int check_act(int act) {
+  return act == RIB_ACT_NONE || act == RIB_ACT_GELU || act == RIB_ACT_SILU ? RIB_OK : RIB_ERR_ARG;
+}
+
+int div_up(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+// How many items the row tiles of one column tile are dealt to: the count
+// with the fewest tiles on the busiest CTA, the smallest such (fewer items
+// reload fewer weights).
+int pick_splits(int m_tiles, int n_tiles, int sms) {
+  int best = 1;
+  long long best_cost = -1;
+  for (int s = 1; s <= m_tiles && s <= 2 * sms; ++s) {
+    const long long cost =
+        (long long)div_up((long long)n_tiles * s, sms) * div_up(m_tiles, s);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct GemmPlan {
+  int bn, m_tiles, n_tiles, splits, k_steps, stages, grid;
+  bool resident;
+  size_t smem;
+};
+
+GemmPlan plan_gemm(int M, int N, int K, bool gated, int sms) {
+  GemmPlan g{};
+  g.m_tiles = div_up(M, 128);
+  g.k_steps = div_up(K, 64);
+  const int unit = gated ? 128 : 64;             // bn is a multiple of this
+  const int cols = gated ? 2 * N : N;
+  // the widest tiles that split the columns evenly, narrower ones while
+  // there are SMs without a tile
+  const int n = div_up(cols, 256);
+  g.bn = div_up(div_up(cols, n), unit) * unit;
+  while (g.bn > unit && (long long)g.m_tiles * div_up(cols, g.bn) < sms) g.bn -= unit;
+  g.n_tiles = div_up(cols, g.bn);
+  g.splits = pick_splits(g.m_tiles, g.n_tiles, sms);
+  const int items = g.n_tiles * g.splits;
+  g.grid = items < sms ? items : sms;
+  const size_t b = (size_t)g.bn * 128;
+  const size_t room = kSmemMax - gemm_smem_bytes(0, 0, 0, false);
+  // weights stay in shared memory over an item's row tiles when at least
+  // four stages of x still fit beside them
+  g.resident = g.m_tiles >= 2 * g.splits && g.k_steps * b + 4 * kGemmATile <= room;
+  const size_t left = room - (g.resident ? g.k_steps * b : 0);
+  g.stages = static_cast<int>(left / (kGemmATile + (g.resident ? 0 : b)));
+  if (g.stages > kGemmMaxStages) g.stages = kGemmMaxStages;
+  g.smem = gemm_smem_bytes(g.bn, g.stages, g.k_steps, g.resident);
+  return g;
+}
+
+// bf16 [rows][cols] as a 2-D map with boxes of box_cols x box_rows
+int map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
+           uint32_t box_rows, CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const uint64_t dims[2] = {cols, rows};
+  const uint64_t strides[1] = {2 * cols};
+  const uint32_t box[2] = {box_cols, box_rows};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, sw);
+}
+
+template <int MODE, int ACT>
+int launch_gemm(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
+                const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
+  CUtensorMap ta, tb, ty, tp;
+  int rc = map_2d(&ta, a, M, K, 64, 128);
+  if (!rc)
+    rc = MODE == kLinear ? map_2d(&tb, b, N, K, 64, g.bn)
+         : MODE == kGated ? map_2d(&tb, b, 2ull * N, K, 64, g.bn / 2)
+                          : map_2d(&tb, b, K, N, 64, 64);
+  if (!rc) rc = map_2d(&ty, y, M, N, 64, 32);
+  if (!rc) rc = map_2d(&tp, pre ? pre : y, M, N, 64, 32);
+  if (rc) return rc;
+  GemmParams p{};
+  p.bias = bias;
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.has_pre = pre != nullptr;
+  p.M = M; p.N = N; p.K = K;
+  p.bn = g.bn;
+  p.m_tiles = g.m_tiles; p.n_tiles = g.n_tiles; p.splits = g.splits;
+  p.k_steps = g.k_steps; p.stages = g.stages; p.b_resident = g.resident;
+  p.wait_limit_ns = g_wait_limit_ns;
+  if ((rc = set_smem(gemm_kernel<MODE, ACT>, g.smem))) return rc;
+  TraceScope ts(kid, st);
+  gemm_kernel<MODE, ACT><<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, p);
+  return launch_status();
+}
+
+template <int MODE>
+int launch_gemm_act(int act, int kid, const GemmPlan& g, const void* a, const void* b,
+                    const float* bias, const void* residual, void* pre, void* y, int M, int N,
+                    int K, cudaStream_t st) {
+  switch (act) {
+    case RIB_ACT_GELU:
+      return launch_gemm<MODE, kActGelu>(kid, g, a, b, bias, residual, pre, y, M, N, K, st);
+    case RIB_ACT_SILU:
+      return launch_gemm<MODE, kActSilu>(kid, g, a, b, bias, residual, pre, y, M, N, K, st);
+    default:
+      return launch_gemm<MODE, kActNone>(kid, g, a, b, bias, residual, pre, y, M, N, K, st);
+  }
+}
+
+struct DwPlan {
+  int m_tiles, n_tiles, splits, steps, per_split;
+  size_t part, part_db;   // bytes
+};
+
+// dW [N][K] over `rows` rows.  More splits shorten the rows' loop and
+// lengthen the sum of the partials: the count with the smallest estimate of
+// both (about 0.6 us per 64-row step of a full tile, 4 TB/s for the partials
+// written and read).
+DwPlan plan_dw(int rows, int N, int K, int sms) {
+  DwPlan d{};
+  d.m_tiles = div_up(N, 256);
+  d.n_tiles = div_up(K, kDwBn);
+  d.steps = div_up(rows, 64);
+  const long long tiles = (long long)d.m_tiles * d.n_tiles;
+  double best = -1.0;
+  for (int s = 1; s <= d.steps && (s == 1 || tiles * s <= 2ll * sms); ++s) {
+    const int per = div_up(d.steps, s);
+    const double cost = div_up(tiles * s, sms) * (per + 4) * 0.6 +
+                        (double)s * N * K * 8.0 / 4.0e6;
+    if (best < 0 || cost < best) {
+      best = cost;
+      d.per_split = per;
+      d.splits = div_up(d.steps, per);   // no empty range
+    }
+  }
+  d.part = align256((size_t)d.splits * N * K * 4);
+  d.part_db = align256((size_t)d.splits * N * 4);
+  return d;
+}
+
+// dW = dz^T x (fp32, or bf16) and, with db, its column sums.
+int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, int K, void* dw,
+              int dw_dtype, float* db, void* part, void* part_db, cudaStream_t st) {
+  CUtensorMap tz, tx;
+  int rc = map_2d(&tz, dz, rows, N, 64, 64);
+  if (!rc) rc = map_2d(&tx, x, rows, K, 64, 64);
+  if (rc) return rc;
+  DwParams p{};
+  p.rows = rows; p.N = N; p.K = K;
+  p.m_tiles = d.m_tiles; p.n_tiles = d.n_tiles; p.splits = d.splits;
+  p.steps = d.steps; p.steps_per_split = d.per_split;
+  p.part = static_cast<float*>(part);
+  p.part_db = db ? static_cast<float*>(part_db) : nullptr;
+  p.wait_limit_ns = g_wait_limit_ns;
+  const size_t smem = dw_smem_bytes();
+  if ((rc = set_smem(dw_kernel, smem))) return rc;
+  {
+    TraceScope ts(K_DW, st);
+    dw_kernel<<<d.m_tiles * d.n_tiles * d.splits, kGemmThreads, smem, st>>>(tz, tx, p);
+    if ((rc = launch_status())) return rc;
+  }
+  {
+    TraceScope ts(K_DW_RED, st);
+    const size_t n = (size_t)N * K;
+    const bool f32 = dw_dtype == RIB_DTYPE_F32;
+    dw_reduce_kernel<<<div_up((long long)n / 4, 256), 256, 0, st>>>(
+        p.part, d.splits, n, f32 ? static_cast<float*>(dw) : nullptr,
+        f32 ? nullptr : static_cast<__nv_bfloat16*>(dw));
+    if ((rc = launch_status())) return rc;
+  }
+  if (db) {
+    TraceScope ts(K_ROWS_RED, st);
+    reduce_rows_kernel<<<div_up(N, 32), kLnThreads, 0, st>>>(p.part_db, d.splits, N, db, 0,
+                                                             nullptr);
+    rc = launch_status();
+  }
+  return rc;
+}
+
+bool aligned16_all(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- layer norm
+
+template <typename T>
+bool ln_vectors(const LnParams& p, int V) {
+  return p.C % V == 0 && aligned16_all({p.x, p.out, p.dy, p.dres});
+}
+
+int ln_grid_rows(int rows, bool cta, int per_warp, int sms, int per_sm) {
+  const long long want = cta ? rows : ((long long)rows + kLnWarps * per_warp - 1) /
+                                          (kLnWarps * per_warp);
+  const long long most = (long long)sms * per_sm;
+  return static_cast<int>(want < most ? want : most);
+}
+
+// Grid of the backward: two CTAs per SM (its registers allow two or three);
+// the CTAs' dgamma / dbeta partials are read back by the reduction, so more
+// CTAs than run at once would only lengthen it.
+int ln_bwd_grid(int rows, int C, int sms) {
+  return ln_grid_rows(rows, C > 1024, 1, sms, 2);
+}
+
+template <typename T, int V, int NV, bool CTA>
+int ln_launch_fwd(const LnParams& p, int sms, cudaStream_t st) {
+  const int grid = ln_grid_rows(p.rows, CTA, ln_rows<V, NV, CTA>(), sms, 8);
+  TraceScope ts(K_LN_FWD, st);
+  layer_norm_fwd_kernel<T, V, NV, CTA><<<grid, kLnThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+template <typename T, int V, int NV, bool CTA>
+int ln_launch_bwd(const LnParams& p, int sms, cudaStream_t st) {
+  const size_t smem = CTA || !p.part ? 0 : (size_t)kLnWarps * 2 * p.C * 4;
+  int rc = set_smem(layer_norm_bwd_kernel<T, V, NV, CTA>, smem);
+  if (rc) return rc;
+  TraceScope ts(K_LN_BWD, st);
+  layer_norm_bwd_kernel<T, V, NV, CTA>
+      <<<ln_bwd_grid(p.rows, p.C, sms), kLnThreads, smem, st>>>(p);
+  return launch_status();
+}
+
+// A row of up to 1024 channels belongs to a warp, a wider one to a CTA; rows
+// of whole 16-byte vectors at 16-byte addresses are read as such, others
+// element by element.
+template <typename T, bool FWD>
+int ln_dispatch(const LnParams& p, int sms, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+#define RIB_LN(v, nv, cta)                                       \
+  return FWD ? ln_launch_fwd<T, v, nv, cta>(p, sms, st) \
+             : ln_launch_bwd<T, v, nv, cta>(p, sms, st)
+  const int C = p.C;
+  if (ln_vectors<T>(p, V)) {
+    if (C <= 32 * V) RIB_LN(V, 1, false);
+    if (C <= 64 * V) RIB_LN(V, 2, false);
+    if (C <= 1024) RIB_LN(V, 32 / V, false);
+    if (C <= 256 * V * 2) RIB_LN(V, 2, true);
+    RIB_LN(V, 32 / V, true);
+  }
+  if (C <= 256) RIB_LN(1, 8, false);
+  if (C <= 1024) RIB_LN(1, 32, false);
+  if (C <= 2048) RIB_LN(1, 8, true);
+  RIB_LN(1, 32, true);
+#undef RIB_LN
+}
+
+int ln_check(int dtype, int rows, int C) {
+  if (dtype != RIB_DTYPE_BF16 && dtype != RIB_DTYPE_F32) return RIB_ERR_ARG;
+  if (rows < 0 || C <= 0) return RIB_ERR_ARG;
+  if (C > kLnMaxC || rows > kMaxRows) return RIB_ERR_UNSUPPORTED;
+  return RIB_OK;
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// ---------------------------------------------------------------- workspaces
+
+int dz_row_splits(int rows, int N, int sms) {
+  const int gx = div_up(N, 256);
+  const int most = std::max(1, 6 * sms / gx);
+  return std::min(div_up(rows, 32), most);
+}
+
+struct LinearBwdWs {
+  size_t dz, part_sum, part_dw, part_db, total;
+  DwPlan dw;
+  int row_splits;
+};
+
+LinearBwdWs linear_bwd_ws(int rows, int K, int N, int act, int sms) {
+  LinearBwdWs w{};
+  w.dw = plan_dw(rows, N, K, sms);
+  w.row_splits = dz_row_splits(rows, N, sms);
+  size_t off = 0;
+  w.dz = off;
+  off = align256(off + (act == RIB_ACT_NONE ? 0 : (size_t)rows * N * 2));
+  w.part_sum = off;
+  off = align256(off + (size_t)w.row_splits * N * 4);
+  w.part_dw = off;
+  off += w.dw.part;
+  w.part_db = off;
+  off += w.dw.part_db;
+  w.total = off;
+  return w;
+}
+
+struct FfnBwdPlan {
+  int m_tiles, n_tiles, splits, k_steps, stages, grid;
+  bool resident;
+  size_t smem;
+};
+
+FfnBwdPlan plan_ffn_bwd(int rows, int C, int H, int sms) {
+  FfnBwdPlan f{};
+  f.m_tiles = div_up(rows, 128);
+  f.n_tiles = div_up(H, kFfnCols);
+  f.k_steps = div_up(C, 64);
+  f.splits = pick_splits(f.m_tiles, f.n_tiles, sms);
+  f.grid = std::min(f.n_tiles * f.splits, sms);
+  const size_t room = kSmemMax - ffn_bwd_smem_bytes(0, 0, false);
+  const size_t b = (size_t)f.k_steps * kFfnB;
+  f.resident = f.m_tiles >= 2 * f.splits && b + 3 * kFfnA <= room;
+  f.stages = static_cast<int>((room - (f.resident ? b : 0)) / (kFfnA + (f.resident ? 0 : kFfnB)));
+  f.stages = std::min(f.stages, kFfnMaxStages);
+  f.smem = ffn_bwd_smem_bytes(f.stages, f.k_steps, f.resident);
+  return f;
+}
+
+struct FfnBwdWs {
+  size_t h, d, part_sum, part_dw, part_db, total;
+  FfnBwdPlan f;
+  DwPlan in, out;
+};
+
+FfnBwdWs ffn_bwd_ws(int rows, int C, int H, int sms) {
+  FfnBwdWs w{};
+  w.f = plan_ffn_bwd(rows, C, H, sms);
+  w.in = plan_dw(rows, 2 * H, C, sms);
+  w.out = plan_dw(rows, C, H, sms);
+  size_t off = 0;
+  w.h = off;
+  off = align256(off + (size_t)rows * H * 2);
+  w.d = off;
+  off = align256(off + (size_t)rows * H * 4);
+  w.part_sum = off;
+  off = align256(off + (size_t)w.f.splits * 8 * H * 4);
+  w.part_dw = off;   // shared by the two weight gradients, one after the other
+  off += std::max(w.in.part, w.out.part);
+  w.part_db = off;
+  off += w.out.part_db;
+  w.total = off;
+  return w;
+}
+
+int check_ffn(int rows, int C, int H) {
+  int rc = check_product(rows, C, H);
+  if (rc) return rc;
+  return 2 * H > kMaxChannels ? RIB_ERR_UNSUPPORTED : RIB_OK;
+}
+
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return RIB_OK;
+  if (!ws || bytes < need) return RIB_ERR_WORKSPACE;
+  return aligned_to(ws, 256) ? RIB_OK : RIB_ERR_ALIGN;
+}
+
+int zero_async(void* p, size_t bytes, cudaStream_t st) {
+  return !p || cudaMemsetAsync(p, 0, bytes, st) == cudaSuccess ? RIB_OK : RIB_ERR_CUDA;
+}
+
+size_t dtype_bytes(int dtype) { return dtype == RIB_DTYPE_F32 ? 4 : 2; }
+
+template <int ACT>
+int launch_dz(const DzParams& p, int row_splits, cudaStream_t st) {
+  TraceScope ts(K_DZ, st);
+  dz_kernel<ACT><<<dim3(div_up(p.N, 256), row_splits), 256, 0, st>>>(p);
+  return launch_status();
+}
+
+template <int ACT>
+int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void* w_in,
+                   const void* w_out, const FfnBwdParams& p, uint8_t* ws, cudaStream_t st) {
+  CUtensorMap tx, ty, ti, to, th, td;
+  int rc = map_2d(&tx, x, p.M, p.C, 64, 128);
+  if (!rc) rc = map_2d(&ty, dy, p.M, p.C, 64, 128);
+  if (!rc) rc = map_2d(&ti, w_in, 2ull * p.H, p.C, 64, 64);
+  if (!rc) rc = map_2d(&to, w_out, p.C, p.H, 64, 64);
+  if (!rc) rc = map_2d(&th, ws + w.h, p.M, p.H, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!rc) {
+    const uint64_t dims[3] = {(uint64_t)p.H, 2, (uint64_t)p.M};
+    const uint64_t strides[2] = {2ull * p.H, 4ull * p.H};
+    const uint32_t box[3] = {32, 1, 32};
+    rc = make_map(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ws + w.d, dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  if (rc) return rc;
+  if ((rc = set_smem(ffn_bwd_kernel<ACT>, w.f.smem))) return rc;
+  TraceScope ts(K_FFN_BWD, st);
+  ffn_bwd_kernel<ACT><<<w.f.grid, kGemmThreads, w.f.smem, st>>>(tx, ty, ti, to, th, td, p);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace rib
+
+extern "C" {
+
+int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* gamma,
+                       const float* beta, float eps, void* y, float* mean, float* rstd,
+                       void* stream) {
+  int rc = ln_check(dtype, rows, C);
+  if (rc) return rc;
+  if (!(eps >= 0.f)) return RIB_ERR_ARG;
+  if (rows == 0) return RIB_OK;
+  if (!x || !y) return RIB_ERR_ARG;
+  const uintptr_t es = dtype_bytes(dtype);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(gamma, 4) || !aligned_to(beta, 4) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return RIB_ERR_ALIGN;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  LnParams p{};
+  p.x = x; p.out = y; p.gamma = gamma; p.beta = beta; p.mean = mean; p.rstd = rstd;
+  p.rows = rows; p.C = C; p.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16, true>(p, sms, st)
+                                 : ln_dispatch<float, true>(p, sms, st);
+}
+
+size_t rib_layer_norm_bwd_workspace(int rows, int C) {
+  int sms = 0;
+  if (ln_check(RIB_DTYPE_BF16, rows, C) || rows == 0 || device_sms(&sms)) return 0;
+  return align256((size_t)ln_bwd_grid(rows, C, sms) * 2 * C * 4);
+}
+
+int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C,
+                       const float* mean, const float* rstd, const float* gamma, const void* dres,
+                       void* dx, float* dgamma, float* dbeta, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int rc = ln_check(dtype, rows, C);
+  if (rc) return rc;
+  if (!aligned_to(dgamma, 4) || !aligned_to(dbeta, 4)) return RIB_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {   // empty sums
+    if ((rc = zero_async(dgamma, (size_t)C * 4, st))) return rc;
+    return zero_async(dbeta, (size_t)C * 4, st);
+  }
+  if (!x || !dy || !mean || !rstd || !dx) return RIB_ERR_ARG;
+  const uintptr_t es = dtype_bytes(dtype);
+  if (!aligned_to(x, es) || !aligned_to(dy, es) || !aligned_to(dx, es) || !aligned_to(dres, es) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(gamma, 4))
+    return RIB_ERR_ALIGN;
+  const bool sums = dgamma || dbeta;
+  if (sums && (rc = check_workspace(workspace, workspace_bytes,
+                                    rib_layer_norm_bwd_workspace(rows, C))))
+    return rc;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  LnParams p{};
+  p.x = x; p.dy = dy; p.dres = dres; p.out = dx; p.gamma = gamma;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.part = sums ? static_cast<float*>(workspace) : nullptr;
+  p.rows = rows; p.C = C;
+  rc = dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16, false>(p, sms, st)
+                               : ln_dispatch<float, false>(p, sms, st);
+  if (rc || !sums) return rc;
+  TraceScope ts(K_ROWS_RED, st);
+  reduce_rows_kernel<<<div_up(2 * C, 32), kLnThreads, 0, st>>>(p.part, ln_bwd_grid(rows, C, sms),
+                                                               C, dgamma, C, dbeta);
+  return launch_status();
+}
+
+int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const float* bias,
+                   int act, const void* residual, void* pre, void* y, void* stream) {
+  int rc = check_product(rows, K, N);
+  if (rc || (rc = check_act(act))) return rc;
+  if (rows == 0) return RIB_OK;
+  if (!x || !w || !y) return RIB_ERR_ARG;
+  if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  const GemmPlan g = plan_gemm(rows, N, K, false, sms);
+  return launch_gemm_act<kLinear>(act, K_LINEAR, g, x, w, bias, residual, pre, y, rows, N, K,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+size_t rib_linear_bwd_workspace(int rows, int K, int N, int act) {
+  int sms = 0;
+  if (check_product(rows, K, N) || check_act(act) || rows == 0 || device_sms(&sms)) return 0;
+  return linear_bwd_ws(rows, K, N, act, sms).total;
+}
+
+int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act, const void* pre,
+                   const void* dy, const void* dx_add, void* dx, void* dw, int dw_dtype, float* db,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_product(rows, K, N);
+  if (rc || (rc = check_act(act))) return rc;
+  if (dw_dtype != RIB_DTYPE_BF16 && dw_dtype != RIB_DTYPE_F32) return RIB_ERR_ARG;
+  if (!aligned16_all({x, w, pre, dy, dx_add, dx, dw, db})) return RIB_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {   // empty sums
+    if ((rc = zero_async(dw, (size_t)N * K * dtype_bytes(dw_dtype), st))) return rc;
+    return zero_async(db, (size_t)N * 4, st);
+  }
+  if (!dy || (dx && !w) || (dw && !x) || (act != RIB_ACT_NONE && !pre)) return RIB_ERR_ARG;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  const LinearBwdWs L = linear_bwd_ws(rows, K, N, act, sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, L.total))) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* dz = dy;
+  // db comes out of the dW product where dz is dy itself; an activation's dz
+  // is summed in fp32 before its rounding, in the kernel that forms it
+  const bool db_in_dw = act == RIB_ACT_NONE && dw;
+  if (act != RIB_ACT_NONE || (db && !db_in_dw)) {
+    DzParams p{};
+    p.dy = static_cast<const __nv_bfloat16*>(dy);
+    p.pre = static_cast<const __nv_bfloat16*>(pre);
+    p.dz = reinterpret_cast<__nv_bfloat16*>(ws + L.dz);
+    p.part = db ? reinterpret_cast<float*>(ws + L.part_sum) : nullptr;
+    p.rows = rows; p.N = N;
+    rc = act == RIB_ACT_GELU   ? launch_dz<kActGelu>(p, L.row_splits, st)
+         : act == RIB_ACT_SILU ? launch_dz<kActSilu>(p, L.row_splits, st)
+                               : launch_dz<kActNone>(p, L.row_splits, st);
+    if (rc) return rc;
+    if (act != RIB_ACT_NONE) dz = p.dz;
+    if (db) {
+      TraceScope ts(K_ROWS_RED, st);
+      reduce_rows_kernel<<<div_up(N, 32), kLnThreads, 0, st>>>(p.part, L.row_splits, N, db, 0,
+                                                               nullptr);
+      if ((rc = launch_status())) return rc;
+    }
+  }
+  if (dx) {
+    const GemmPlan g = plan_gemm(rows, K, N, false, sms);
+    rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, dz, w, nullptr, dx_add, nullptr, dx, rows, K,
+                                    N, st);
+    if (rc) return rc;
+  }
+  if (dw)
+    rc = launch_dw(L.dw, dz, x, rows, N, K, dw, dw_dtype, db_in_dw ? db : nullptr, ws + L.part_dw,
+                   ws + L.part_db, st);
+  return rc;
+}
+
+size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden) {
+  if (check_ffn(rows, C, hidden)) return 0;
+  return align256((size_t)rows * hidden * 2);
+}
+
+int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_in,
+                      const float* b_in, const void* w_out, const float* b_out, int act,
+                      const void* residual, void* y, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  int rc = check_ffn(rows, C, hidden);
+  if (rc || (rc = check_act(act))) return rc;
+  if (rows == 0) return RIB_OK;
+  if (!x || !w_in || !w_out || !y) return RIB_ERR_ARG;
+  if (!aligned16_all({x, w_in, b_in, w_out, b_out, residual, y})) return RIB_ERR_ALIGN;
+  if ((rc = check_workspace(workspace, workspace_bytes,
+                            rib_gated_ffn_fwd_workspace(rows, C, hidden))))
+    return rc;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const GemmPlan g = plan_gemm(rows, hidden, C, true, sms);
+  rc = launch_gemm_act<kGated>(act, K_GATED, g, x, w_in, b_in, nullptr, nullptr, workspace, rows,
+                               hidden, C, st);
+  if (rc) return rc;
+  const GemmPlan o = plan_gemm(rows, C, hidden, false, sms);
+  return launch_gemm<kLinear, kActNone>(K_LINEAR, o, workspace, w_out, b_out, residual, nullptr, y,
+                                        rows, C, hidden, st);
+}
+
+size_t rib_gated_ffn_bwd_workspace(int rows, int C, int hidden) {
+  int sms = 0;
+  if (check_ffn(rows, C, hidden) || rows == 0 || device_sms(&sms)) return 0;
+  return ffn_bwd_ws(rows, C, hidden, sms).total;
+}
+
+int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_in,
+                      const float* b_in, const void* w_out, int act, const void* dy,
+                      const void* dx_add, void* dx, void* dw_in, float* db_in, void* dw_out,
+                      float* db_out, int dw_dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  int rc = check_ffn(rows, C, hidden);
+  if (rc || (rc = check_act(act))) return rc;
+  if (dw_dtype != RIB_DTYPE_BF16 && dw_dtype != RIB_DTYPE_F32) return RIB_ERR_ARG;
+  if (!dw_in || !dw_out) return RIB_ERR_ARG;
+  if (!aligned16_all({x, w_in, b_in, w_out, dy, dx_add, dx, dw_in, db_in, dw_out, db_out}))
+    return RIB_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t es = dtype_bytes(dw_dtype);
+  if (rows == 0) {   // empty sums
+    if ((rc = zero_async(dw_in, 2 * es * hidden * C, st))) return rc;
+    if ((rc = zero_async(db_in, (size_t)hidden * 8, st))) return rc;
+    if ((rc = zero_async(dw_out, es * C * hidden, st))) return rc;
+    return zero_async(db_out, (size_t)C * 4, st);
+  }
+  if (!x || !w_in || !w_out || !dy || !dx) return RIB_ERR_ARG;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  const FfnBwdWs L = ffn_bwd_ws(rows, C, hidden, sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, L.total))) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  FfnBwdParams p{};
+  p.b_in = b_in;
+  p.part = db_in ? reinterpret_cast<float*>(ws + L.part_sum) : nullptr;
+  p.M = rows; p.C = C; p.H = hidden;
+  p.m_tiles = L.f.m_tiles; p.n_tiles = L.f.n_tiles; p.splits = L.f.splits;
+  p.k_steps = L.f.k_steps; p.stages = L.f.stages; p.b_resident = L.f.resident;
+  p.wait_limit_ns = g_wait_limit_ns;
+  rc = act == RIB_ACT_GELU   ? launch_ffn_bwd<kActGelu>(L, x, dy, w_in, w_out, p, ws, st)
+       : act == RIB_ACT_SILU ? launch_ffn_bwd<kActSilu>(L, x, dy, w_in, w_out, p, ws, st)
+                             : launch_ffn_bwd<kActNone>(L, x, dy, w_in, w_out, p, ws, st);
+  if (rc) return rc;
+  if (db_in) {
+    TraceScope ts(K_ROWS_RED, st);
+    reduce_rows_kernel<<<div_up(2 * hidden, 32), kLnThreads, 0, st>>>(
+        p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr);
+    if ((rc = launch_status())) return rc;
+  }
+  const GemmPlan g = plan_gemm(rows, C, 2 * hidden, false, sms);
+  rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, ws + L.d, w_in, nullptr, dx_add, nullptr, dx,
+                                  rows, C, 2 * hidden, st);
+  if (rc) return rc;
+  if ((rc = launch_dw(L.in, ws + L.d, x, rows, 2 * hidden, C, dw_in, dw_dtype, nullptr,
+                      ws + L.part_dw, nullptr, st)))
+    return rc;
+  return launch_dw(L.out, dy, ws + L.h, rows, C, hidden, dw_out, dw_dtype, db_out, ws + L.part_dw,
+                   ws + L.part_db, st);
+}
+
+}  // extern "C"

@@ -26,6 +26,7 @@
 #include "attn_bwd_persist.cuh"
 #include "cla.cuh"
 #include "cla_bwd.cuh"
+#include "layer_kernels.cuh"
 
 namespace rib {
 namespace {
@@ -142,7 +143,11 @@ int map_pixel_f32(CUtensorMap* m, const void* base, int B, int heads, int H, int
 // ---------------------------------------------------------------- tracing
 enum KernelId {
   K_POS, K_FWD, K_BWD_PRE, K_BWD, K_DQ_FIN, K_POSGRAD, K_MLP_PART, K_MLP_RED, K_COPY, K_DEBUG,
-  K_CLA, K_CLA_DZ, K_CLA_DWPW, K_CLA_DX, K_CLA_RED, K_BWD_PERSIST, K_FWD_TF32, K_CLA_DY, K_COUNT
+  K_CLA, K_CLA_DZ, K_CLA_DWPW, K_CLA_DX, K_CLA_RED, K_BWD_PERSIST, K_FWD_TF32, K_CLA_DY,
+#define RIB_KERNEL_ID(id, name) id,
+  RIB_LAYER_KERNELS(RIB_KERNEL_ID)
+#undef RIB_KERNEL_ID
+  K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "pos_tokens_kernel",   "attn_fwd_kernel",        "bwd_preprocess_kernel",
@@ -150,7 +155,11 @@ const char* const kKernelNames[K_COUNT] = {
     "mlp_bwd_partial_kernel", "mlp_bwd_reduce_kernel", "window_copy_kernel",
     "debug_wait_kernel",   "cla_gate_kernel",        "cla_bwd_dz_kernel",
     "cla_bwd_dwpw_kernel", "cla_bwd_dx_kernel",      "cla_bwd_reduce_kernel",
-    "attn_bwd_persistent_kernel", "attn_fwd_tf32_kernel", "cla_bwd_dy_kernel"};
+    "attn_bwd_persistent_kernel", "attn_fwd_tf32_kernel", "cla_bwd_dy_kernel",
+#define RIB_KERNEL_NAME(id, name) name,
+    RIB_LAYER_KERNELS(RIB_KERNEL_NAME)
+#undef RIB_KERNEL_NAME
+};
 
 struct TraceRec {
   int id;
@@ -1207,3 +1216,6 @@ int rib_window_scatter(const void* xw, int B, int H, int W, int C, int elem_byte
 }
 
 }  // extern "C"
+
+// the layer norm, linear and feed-forward entry points
+#include "layer_api.cuh"
