@@ -7,9 +7,11 @@ element in fp64 beside the reference:
   U = 2^-24   one rounding to fp32; an accumulation of n products on the
               tensor cores adds at most (n / 16 + 24) sums that may truncate,
               2 U each, times the sum of the products' magnitudes
-  the activations' errors as their formulas give them: gelu's Q to 1.5e-7 / 2
-  and a few ulps of the approximate exponential and reciprocal, silu's
-  logistic to those ulps and the rounded exponent
+  the activations' errors as their formulas give them: gelu's value is
+  max(z, 0) - |z| Q with Q to 0.081 (2^-12 Q + 1e-7) by the fit of its
+  polynomial, and below 1e-9 beyond |z| = 6; its slope takes Q to 1.5e-7 / 2;
+  silu's logistic and every exponential and reciprocal add a few ulps and the
+  exponent's own rounding
 Where at least 4096 elements were rounded, the 2-norm error has to be that of
 independent roundings too: each has an rms of at most H / sqrt 3, so two of
 them stay below H.
@@ -61,7 +63,8 @@ def _mma(n):
 
 def _act_err(z, act):
     if act == "gelu":
-        return 6e-7 * np.abs(z)
+        q = O.act_value(-np.abs(z), act) / -np.maximum(np.abs(z), 1e-30)
+        return np.abs(z) * (1e-8 + (0.081 * 2.0 ** -12 + 1e-5) * q + 2 * U * (z >= 0))
     if act == "silu":
         return (np.abs(z) + 8) * 4 * U * np.abs(O.act_value(z, act))
     return 0 * z

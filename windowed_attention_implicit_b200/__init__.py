@@ -22,6 +22,12 @@ import torch
 
 from . import _abi
 
+try:   # the current stream's handle without a Stream object around it
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:   # pragma: no cover - a torch build without it
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
 __all__ = [
     "RibError", "PositionMLP", "PositionMLPGrad", "PosTokenCache", "rib_pos_tokens",
     "rib_pos_tokens_bwd", "rib_pos_tokens_bwd_workspace", "rib_pos_tokens_bwd_noalloc",
@@ -515,59 +521,113 @@ _MAX_ROWS = 1 << 30
 
 
 def _act(where: str, act: str) -> int:
-    if act not in _ACTS:
+    a = _ACTS.get(act)
+    if a is None:
         raise RibError(_abi.RIB_ERR_ARG, f"{where}: act {act!r} is none of {', '.join(_ACTS)}")
-    return _ACTS[act]
+    return a
 
 
 def _dtype(where: str, name: str, dtype: torch.dtype) -> int:
-    if dtype not in _DTYPES:
+    d = _DTYPES.get(dtype)
+    if d is None:
         raise RibError(_abi.RIB_ERR_UNSUPPORTED, f"{where}: {name} is {dtype}, not bfloat16 or float32")
-    return _DTYPES[dtype]
+    return d
 
 
-def _rows(where: str, x: torch.Tensor, name: str = "x") -> Tuple[int, int]:
-    """x [..., C] seen as rows of C channels."""
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise RibError(_abi.RIB_ERR_ARG, f"{where}: {name} must be [..., channels]")
-    rows = x.numel() // x.shape[-1]
-    if rows > _MAX_ROWS:
-        raise RibError(_abi.RIB_ERR_UNSUPPORTED, f"{where}: {rows} rows, more than 2^30")
-    return rows, x.shape[-1]
+class _Call:
+    """One call of a layer operator: its device, its stream and the checks of
+    its tensors.  Small maps are bound by what happens on the host, so every
+    tensor is looked at once.
 
-
-class _on:
-    """What a call allocates for itself (missing outputs, workspace) belongs to
+    What a call allocates for itself (missing outputs, workspace) belongs to
     the stream that the call runs on, also when that is not torch's current
     one: memory of the current stream could still be in use by work queued
     there, and could be handed out again while the call runs."""
+    __slots__ = ("where", "x", "device", "index", "rows", "channels", "stream", "side")
 
-    def __init__(self, stream, device):
-        self.current = torch.cuda.current_stream(device) if device.type == "cuda" else None
+    def __init__(self, where: str, x: torch.Tensor, stream):
+        self.where, self.x = where, x
+        if x.dim() < 1 or x.shape[-1] == 0:
+            raise RibError(_abi.RIB_ERR_ARG, f"{where}: x must be [..., channels]")
+        self.channels = x.shape[-1]
+        self.rows = x.numel() // self.channels
+        if self.rows > _MAX_ROWS:
+            raise RibError(_abi.RIB_ERR_UNSUPPORTED, f"{where}: {self.rows} rows, more than 2^30")
+        self.device, self.index = x.device, x.get_device()
         self.side = None
-        if stream is not None and self.current is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.cuda_stream != self.current.cuda_stream:
-                self.side = stream
+        self.stream = 0
+        if self.index >= 0:
+            if self.index != torch.cuda.current_device():
+                raise RibError(_abi.RIB_ERR_ARG, f"{where}: tensors are on {x.device}, the current "
+                               f"device is cuda:{torch.cuda.current_device()}")
+            self.stream = _raw_stream(self.index)
+            if stream is not None:
+                if not hasattr(stream, "cuda_stream"):
+                    stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+                if stream.cuda_stream != self.stream:
+                    self.side, self.stream = stream, stream.cuda_stream
 
-    def empty(self, shape, device, dtype) -> torch.Tensor:
+    def empty(self, shape, dtype) -> torch.Tensor:
         if self.side is None:
-            return torch.empty(shape, device=device, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.side):
-            return torch.empty(shape, device=device, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def output(self, given, shape, device, dtype) -> torch.Tensor:
-        """An output the caller will use on the current stream."""
+    def output(self, given, shape, dtype) -> torch.Tensor:
+        """An output, allocated if it was not given; the caller will use it on
+        the current stream."""
         if given is not None:
             return given
-        t = self.empty(shape, device, dtype)
-        if self.side is not None:
-            t.record_stream(self.current)
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        t = self.empty(shape, dtype)
+        t.record_stream(torch.cuda.current_stream())
         return t
 
-    def workspace(self, given, need, device) -> torch.Tensor:
-        return self.empty(max(need, 256), device, torch.uint8) if given is None else given
+    def like_x(self, given) -> torch.Tensor:
+        if given is not None:
+            return given
+        if self.side is None:
+            return torch.empty_like(self.x, memory_format=torch.contiguous_format)
+        return self.output(None, self.x.shape, self.x.dtype)
+
+    def ptr(self, name: str, t: Optional[torch.Tensor], n: int, dtype=None) -> Optional[int]:
+        """Address of a buffer that has to hold exactly n elements of dtype on
+        the call's device (the library takes bare pointers and can check
+        neither); None for None."""
+        if t is None:
+            return None
+        if t.numel() != n:
+            raise RibError(_abi.RIB_ERR_ARG,
+                           f"{self.where}: {name} holds {t.numel()} elements, the call needs {n}")
+        if t.get_device() != self.index or (self.index < 0 and t.device != self.device):
+            raise RibError(_abi.RIB_ERR_ARG,
+                           f"{self.where}: {name} is on {t.device}, not {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        return t.data_ptr()
+
+    def workspace(self, given: Optional[torch.Tensor], need: int):
+        """(address, bytes) of the workspace, allocated if it was not given.
+        After the tensors' checks: the first thing that needs a CUDA tensor."""
+        if self.index < 0:
+            raise ValueError("x must be a CUDA tensor")
+        if given is None:
+            given = self.empty(max(need, 256), torch.uint8)
+        return (self.ptr("workspace", given, given.numel()), given.numel() * given.element_size(),
+                given)
+
+    def run(self, *args) -> None:
+        if self.index < 0:
+            raise ValueError("x must be a CUDA tensor")
+        code = getattr(library(), self.where)(*args, self.stream)
+        if code != _abi.RIB_OK:
+            raise RibError(code, self.where)
+
+
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def rib_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
@@ -575,19 +635,14 @@ def rib_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
                        rstd=None, stream=None):
     """(y, mean, rstd): layer norm of x [..., C] (bf16 or fp32) over its last
     axis, y like x, mean and rstd fp32 [...].  gamma, beta fp32 [C] or None."""
-    name = "rib_layer_norm_fwd"
-    rows, C = _rows(name, x)
-    dt, dev, on = _dtype(name, "x", x.dtype), x.device, _on(stream, x.device)
-    y = on.output(y, x.shape, dev, x.dtype)
-    mean = on.output(mean, x.shape[:-1], dev, torch.float32)
-    rstd = on.output(rstd, x.shape[:-1], dev, torch.float32)
-    _sizes(name, dev, y=(y, x.numel()), mean=(mean, rows), rstd=(rstd, rows), gamma=(gamma, C),
-           beta=(beta, C))
-    f32 = torch.float32
-    _check(library().rib_layer_norm_fwd(
-        _ptr(x, x.dtype, "x"), dt, rows, C, _ptr(gamma, f32, "gamma"), _ptr(beta, f32, "beta"),
-        float(eps), _ptr(y, x.dtype, "y"), _ptr(mean, f32, "mean"), _ptr(rstd, f32, "rstd"),
-        _stream(stream)), name)
+    c = _Call("rib_layer_norm_fwd", x, stream)
+    dtype, rows, C = x.dtype, c.rows, c.channels
+    dt, n, lead = _dtype(c.where, "x", dtype), c.rows * c.channels, x.shape[:-1]
+    y = c.like_x(y)
+    mean, rstd = c.output(mean, lead, _F32), c.output(rstd, lead, _F32)
+    c.run(c.ptr("x", x, n), dt, rows, C, c.ptr("gamma", gamma, C, _F32),
+          c.ptr("beta", beta, C, _F32), float(eps), c.ptr("y", y, n, dtype),
+          c.ptr("mean", mean, rows, _F32), c.ptr("rstd", rstd, rows, _F32))
     return y, mean, rstd
 
 
@@ -602,27 +657,22 @@ def rib_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rs
     """dict(dx, dgamma, dbeta) of rib_layer_norm_fwd.  dres: a second gradient
     of x (the residual path's), added to dx before its rounding.  Without
     weight_grads dgamma and dbeta are None."""
-    name = "rib_layer_norm_bwd"
-    rows, C = _rows(name, x)
-    dt, dev, on = _dtype(name, "x", x.dtype), x.device, _on(stream, x.device)
-    dx = on.output(dx, x.shape, dev, x.dtype)
+    c = _Call("rib_layer_norm_bwd", x, stream)
+    dtype, rows, C = x.dtype, c.rows, c.channels
+    dt, n = _dtype(c.where, "x", dtype), c.rows * c.channels
+    dx = c.like_x(dx)
     if weight_grads:
-        dgamma = on.output(dgamma, (C,), dev, torch.float32)
-        dbeta = on.output(dbeta, (C,), dev, torch.float32)
+        dgamma, dbeta = c.output(dgamma, (C,), _F32), c.output(dbeta, (C,), _F32)
     else:
         dgamma = dbeta = None
-    n = x.numel()
-    _sizes(name, dev, dy=(dy, n), mean=(mean, rows), rstd=(rstd, rows), gamma=(gamma, C),
-           dres=(dres, n), dx=(dx, n), dgamma=(dgamma, C), dbeta=(dbeta, C))
-    f32 = torch.float32
-    ptrs = [_ptr(x, x.dtype, "x"), _ptr(dy, x.dtype, "dy")]
-    workspace = on.workspace(workspace, rib_layer_norm_bwd_workspace(rows, C) if weight_grads else 0,
-                             dev)
-    _check(library().rib_layer_norm_bwd(
-        *ptrs, dt, rows, C, _ptr(mean, f32, "mean"), _ptr(rstd, f32, "rstd"),
-        _ptr(gamma, f32, "gamma"), _ptr(dres, x.dtype, "dres"), _ptr(dx, x.dtype, "dx"),
-        _ptr(dgamma, f32, "dgamma"), _ptr(dbeta, f32, "dbeta"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+    args = (c.ptr("x", x, n), c.ptr("dy", dy, n, dtype), dt, rows, C,
+            c.ptr("mean", mean, rows, _F32), c.ptr("rstd", rstd, rows, _F32),
+            c.ptr("gamma", gamma, C, _F32), c.ptr("dres", dres, n, dtype),
+            c.ptr("dx", dx, n, dtype), c.ptr("dgamma", dgamma, C, _F32),
+            c.ptr("dbeta", dbeta, C, _F32))
+    need = rib_layer_norm_bwd_workspace(rows, C) if weight_grads and workspace is None else 0
+    ws, size, _keep = c.workspace(workspace, need)
+    c.run(*args, ws, size)
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
@@ -639,19 +689,15 @@ def rib_linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     [N][K], bias fp32 [N]; act "none", "gelu" (erf form) or "silu".  pre is
     the bf16 x w^T + bias that the backward of an activation needs, when
     save_pre (or a buffer for it) is given, else None."""
-    name, bf = "rib_linear_fwd", torch.bfloat16
-    rows, K = _rows(name, x)
-    N = _weight(name, w, K)
-    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
-    shape = (*x.shape[:-1], N)
-    y = on.output(y, shape, dev, bf)
-    pre = on.output(pre, shape, dev, bf) if save_pre or pre is not None else None
-    _sizes(name, dev, w=(w, N * K), bias=(bias, N), residual=(residual, rows * N), y=(y, rows * N),
-           pre=(pre, rows * N))
-    _check(library().rib_linear_fwd(
-        _ptr(x, bf, "x"), rows, K, _ptr(w, bf, "w"), N, _ptr(bias, torch.float32, "bias"), a,
-        _ptr(residual, bf, "residual"), _ptr(pre, bf, "pre"), _ptr(y, bf, "y"), _stream(stream)),
-        name)
+    c = _Call("rib_linear_fwd", x, stream)
+    rows, K = c.rows, c.channels
+    N, a = _weight(c.where, w, K), _act(c.where, act)
+    shape, n = (*x.shape[:-1], N), c.rows * N
+    y = c.output(y, shape, _BF16)
+    pre = c.output(pre, shape, _BF16) if save_pre or pre is not None else None
+    c.run(c.ptr("x", x, rows * K, _BF16), rows, K, c.ptr("w", w, N * K, _BF16), N,
+          c.ptr("bias", bias, N, _F32), a, c.ptr("residual", residual, n, _BF16),
+          c.ptr("pre", pre, n, _BF16), c.ptr("y", y, n, _BF16))
     return y, pre
 
 
@@ -669,25 +715,24 @@ def rib_linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, act: str 
     wanted (with_dx, with_dw, with_db) is None.  dx_add: a second gradient of x,
     added to dx before its rounding.  dw is fp32 or bf16 (dw_dtype, or the type
     of the buffer given)."""
-    name, bf = "rib_linear_bwd", torch.bfloat16
-    rows, K = _rows(name, x)
-    N = _weight(name, w, K)
-    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    c = _Call("rib_linear_bwd", x, stream)
+    rows, K = c.rows, c.channels
+    N, a = _weight(c.where, w, K), _act(c.where, act)
     if a != _abi.RIB_ACT_NONE and pre is None:
-        raise RibError(_abi.RIB_ERR_ARG, f"{name}: act {act!r} needs pre (rib_linear_fwd's, with save_pre)")
-    dx = on.output(dx, x.shape, dev, bf) if with_dx else None
-    dw = on.output(dw, (N, K), dev, dw_dtype) if with_dw else None
-    db = on.output(db, (N,), dev, torch.float32) if with_db else None
-    dt = _dtype(name, "dw", dw.dtype) if dw is not None else _abi.RIB_DTYPE_F32
-    _sizes(name, dev, w=(w, N * K), dy=(dy, rows * N), pre=(pre, rows * N), dx_add=(dx_add, rows * K),
-           dx=(dx, rows * K), dw=(dw, N * K), db=(db, N))
-    xp = _ptr(x, bf, "x")
-    workspace = on.workspace(workspace, rib_linear_bwd_workspace(rows, K, N, act), dev)
-    _check(library().rib_linear_bwd(
-        xp, rows, K, _ptr(w, bf, "w"), N, a, _ptr(pre, bf, "pre"), _ptr(dy, bf, "dy"),
-        _ptr(dx_add, bf, "dx_add"), _ptr(dx, bf, "dx"), _ptr(dw, None, "dw"), dt,
-        _ptr(db, torch.float32, "db"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+        raise RibError(_abi.RIB_ERR_ARG,
+                       f"{c.where}: act {act!r} needs pre (rib_linear_fwd's, with save_pre)")
+    dw_dtype = dw.dtype if dw is not None else dw_dtype
+    dt = _dtype(c.where, "dw", dw_dtype)
+    dx = c.like_x(dx) if with_dx else None
+    dw = c.output(dw, (N, K), dw_dtype) if with_dw else None
+    db = c.output(db, (N,), _F32) if with_db else None
+    args = (c.ptr("x", x, rows * K, _BF16), rows, K, c.ptr("w", w, N * K, _BF16), N, a,
+            c.ptr("pre", pre, rows * N, _BF16), c.ptr("dy", dy, rows * N, _BF16),
+            c.ptr("dx_add", dx_add, rows * K, _BF16), c.ptr("dx", dx, rows * K, _BF16),
+            c.ptr("dw", dw, N * K), dt, c.ptr("db", db, N, _F32))
+    need = rib_linear_bwd_workspace(rows, K, N, act) if workspace is None else 0
+    ws, size, _keep = c.workspace(workspace, need)
+    c.run(*args, ws, size)
     return {"dx": dx, "dw": dw, "db": db}
 
 
@@ -714,16 +759,13 @@ class GatedFfn:
         return self.w_in.shape[1]
 
 
-def _ffn_sizes(where: str, ffn: GatedFfn, C: int):
-    if ffn.w_in.dim() != 3 or ffn.w_in.shape[0] != 2 or ffn.w_in.shape[2] != C:
-        raise RibError(_abi.RIB_ERR_ARG,
-                       f"{where}: w_in must be [2][hidden][{C}], got {tuple(ffn.w_in.shape)}")
-    H = ffn.hidden
-    if tuple(ffn.w_out.shape) != (C, H):
-        raise RibError(_abi.RIB_ERR_ARG,
-                       f"{where}: w_out must be [{C}][{H}], got {tuple(ffn.w_out.shape)}")
-    return H, {"w_in": (ffn.w_in, 2 * H * C), "b_in": (ffn.b_in, 2 * H), "w_out": (ffn.w_out, C * H),
-               "b_out": (ffn.b_out, C)}
+def _ffn_hidden(where: str, ffn: GatedFfn, C: int) -> int:
+    s, o = ffn.w_in.shape, ffn.w_out.shape
+    if len(s) != 3 or s[0] != 2 or s[2] != C:
+        raise RibError(_abi.RIB_ERR_ARG, f"{where}: w_in must be [2][hidden][{C}], got {tuple(s)}")
+    if len(o) != 2 or o[0] != C or o[1] != s[1]:
+        raise RibError(_abi.RIB_ERR_ARG, f"{where}: w_out must be [{C}][{s[1]}], got {tuple(o)}")
+    return s[1]
 
 
 def rib_gated_ffn_fwd_workspace(rows: int, C: int, hidden: int) -> int:
@@ -735,19 +777,17 @@ def rib_gated_ffn_fwd(x: torch.Tensor, ffn: GatedFfn, act: str = "silu",
                       stream=None) -> torch.Tensor:
     """y = (act(x Wg^T + bg) * (x Wu^T + bu)) Wo^T + b_out + residual for x
     bf16 [..., C]."""
-    name, bf, f32 = "rib_gated_ffn_fwd", torch.bfloat16, torch.float32
-    rows, C = _rows(name, x)
-    H, sizes = _ffn_sizes(name, ffn, C)
-    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
-    y = on.output(y, x.shape, dev, bf)
-    _sizes(name, dev, residual=(residual, rows * C), y=(y, rows * C), **sizes)
-    xp = _ptr(x, bf, "x")
-    workspace = on.workspace(workspace, rib_gated_ffn_fwd_workspace(rows, C, H), dev)
-    _check(library().rib_gated_ffn_fwd(
-        xp, rows, C, H, _ptr(ffn.w_in, bf, "w_in"), _ptr(ffn.b_in, f32, "b_in"),
-        _ptr(ffn.w_out, bf, "w_out"), _ptr(ffn.b_out, f32, "b_out"), a,
-        _ptr(residual, bf, "residual"), _ptr(y, bf, "y"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), name)
+    c = _Call("rib_gated_ffn_fwd", x, stream)
+    rows, C, n = c.rows, c.channels, c.rows * c.channels
+    H, a = _ffn_hidden(c.where, ffn, C), _act(c.where, act)
+    y = c.like_x(y)
+    args = (c.ptr("x", x, n, _BF16), rows, C, H, c.ptr("w_in", ffn.w_in, 2 * H * C, _BF16),
+            c.ptr("b_in", ffn.b_in, 2 * H, _F32), c.ptr("w_out", ffn.w_out, C * H, _BF16),
+            c.ptr("b_out", ffn.b_out, C, _F32), a, c.ptr("residual", residual, n, _BF16),
+            c.ptr("y", y, n, _BF16))
+    need = rib_gated_ffn_fwd_workspace(rows, C, H) if workspace is None else 0
+    ws, size, _keep = c.workspace(workspace, need)
+    c.run(*args, ws, size)
     return y
 
 
@@ -763,32 +803,28 @@ def rib_gated_ffn_bwd(x: torch.Tensor, ffn: GatedFfn, dy: torch.Tensor, act: str
     alone (the residual's gradient is dy: pass it as dx_add where the
     residual is x itself).  db_in and db_out are formed where the block has
     that bias, else None; dw_in and dw_out are both fp32 or both bf16."""
-    name, bf, f32 = "rib_gated_ffn_bwd", torch.bfloat16, torch.float32
-    rows, C = _rows(name, x)
-    H, sizes = _ffn_sizes(name, ffn, C)
-    a, dev, on = _act(name, act), x.device, _on(stream, x.device)
+    c = _Call("rib_gated_ffn_bwd", x, stream)
+    rows, C, n = c.rows, c.channels, c.rows * c.channels
+    H, a = _ffn_hidden(c.where, ffn, C), _act(c.where, act)
     if dw_in is not None:
         dw_dtype = dw_in.dtype
     elif dw_out is not None:
         dw_dtype = dw_out.dtype
-    dt = _dtype(name, "dw_in / dw_out", dw_dtype)
-    dx = on.output(dx, x.shape, dev, bf)
-    dw_in = on.output(dw_in, (2, H, C), dev, dw_dtype)
-    dw_out = on.output(dw_out, (C, H), dev, dw_dtype)
-    db_in = on.output(db_in, (2, H), dev, f32) if ffn.b_in is not None else None
-    db_out = on.output(db_out, (C,), dev, f32) if ffn.b_out is not None else None
-    _sizes(name, dev, dy=(dy, rows * C), dx_add=(dx_add, rows * C), dx=(dx, rows * C),
-           dw_in=(dw_in, 2 * H * C), dw_out=(dw_out, C * H), db_in=(db_in, 2 * H),
-           db_out=(db_out, C), **sizes)
-    xp = _ptr(x, bf, "x")
-    workspace = on.workspace(workspace, rib_gated_ffn_bwd_workspace(rows, C, H), dev)
-    _check(library().rib_gated_ffn_bwd(
-        xp, rows, C, H, _ptr(ffn.w_in, bf, "w_in"), _ptr(ffn.b_in, f32, "b_in"),
-        _ptr(ffn.w_out, bf, "w_out"), a, _ptr(dy, bf, "dy"), _ptr(dx_add, bf, "dx_add"),
-        _ptr(dx, bf, "dx"), _ptr(dw_in, dw_dtype, "dw_in"), _ptr(db_in, f32, "db_in"),
-        _ptr(dw_out, dw_dtype, "dw_out"), _ptr(db_out, f32, "db_out"), dt,
-        _ptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)), name)
+    dt = _dtype(c.where, "dw_in / dw_out", dw_dtype)
+    dx = c.like_x(dx)
+    dw_in = c.output(dw_in, (2, H, C), dw_dtype)
+    dw_out = c.output(dw_out, (C, H), dw_dtype)
+    db_in = c.output(db_in, (2, H), _F32) if ffn.b_in is not None else None
+    db_out = c.output(db_out, (C,), _F32) if ffn.b_out is not None else None
+    c.ptr("b_out", ffn.b_out, C, _F32)   # its values are not needed, its size is
+    args = (c.ptr("x", x, n, _BF16), rows, C, H, c.ptr("w_in", ffn.w_in, 2 * H * C, _BF16),
+            c.ptr("b_in", ffn.b_in, 2 * H, _F32), c.ptr("w_out", ffn.w_out, C * H, _BF16), a,
+            c.ptr("dy", dy, n, _BF16), c.ptr("dx_add", dx_add, n, _BF16), c.ptr("dx", dx, n, _BF16),
+            c.ptr("dw_in", dw_in, 2 * H * C, dw_dtype), c.ptr("db_in", db_in, 2 * H, _F32),
+            c.ptr("dw_out", dw_out, C * H, dw_dtype), c.ptr("db_out", db_out, C, _F32), dt)
+    need = rib_gated_ffn_bwd_workspace(rows, C, H) if workspace is None else 0
+    ws, size, _keep = c.workspace(workspace, need)
+    c.run(*args, ws, size)
     return {"dx": dx, "dw_in": dw_in, "db_in": db_in, "dw_out": dw_out, "db_out": db_out}
 
 

@@ -18,6 +18,7 @@
 
 namespace rib {
 
+constexpr int kFfnThreads = 320;
 constexpr int kFfnCols = 64;                              // hidden channels of a tile
 constexpr uint32_t kFfnA = 2u * kGemmATile;               // x and dy, 64 channels deep
 constexpr uint32_t kFfnB = 3u * 8192u;                    // Wg, Wu (K-major), Wo (MN-major)
@@ -77,7 +78,7 @@ __device__ __forceinline__ void ffn_load_b(uint8_t* dst, const CUtensorMap* tm_i
 // 64 (all 128-byte swizzle); tm_h: h [M][H], boxes 32 x 32, tm_d: dg | du
 // [M][2][H], boxes 32 x 1 x 32 (64-byte swizzle).
 template <int ACT>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x,
                    const __grid_constant__ CUtensorMap tm_dy,
                    const __grid_constant__ CUtensorMap tm_in,

@@ -7,9 +7,9 @@
 //   kGated    y = act(x Wg^T + bg) (x Wu^T + bu)       (W [2][N][K])
 //   dw_kernel dW = dz^T x, db = sum_rows dz            (dz [R][N], x [R][K])
 //
-// gemm_kernel is persistent and warp-specialised: warp 8 feeds a ring of
-// 64-deep operand tiles by TMA, warp 9 issues the MMAs of 128 x bn tiles
-// into one of two accumulators in tensor memory, warps 0-7 are the epilogue
+// gemm_kernel is persistent and warp-specialised: warp 16 feeds a ring of
+// 64-deep operand tiles by TMA, warp 17 issues the MMAs of 128 x bn tiles
+// into one of two accumulators in tensor memory, warps 0-15 are the epilogue
 // of the other one.  Operand tiles are rows of 128 bytes in the 128-byte
 // swizzle, the layout the tensor core reads without bank conflicts; rows and
 // channels outside the matrices are the TMA's zero fill, and outputs outside
@@ -22,7 +22,7 @@
 namespace rib {
 
 constexpr int SITE_GEMM = 50, SITE_DW = 51, SITE_FFN = 52;
-constexpr int G_GEMM_RES = 170, G_GEMM_BIAS = 171, G_DW_PART = 172, G_DW_RED = 173,
+constexpr int G_GEMM_BIAS = 171, G_DW_PART = 172, G_DW_RED = 173,
               G_DZ_IN = 174, G_DZ_OUT = 175, G_FFN_PART = 176;
 
 enum GemmMode { kLinear = 0, kDx = 1, kGated = 2 };
@@ -63,48 +63,86 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// gelu(z) = z Phi(z), Phi the normal distribution function.  With t = |z| /
-// sqrt 2 and k = 1 / (1 + p t), Abramowitz and Stegun's formula 7.1.26 gives
-// erfc(t) = (a1 k + ... + a5 k^5) e^(-t^2) to 1.5e-7, so with Q = erfc(t) / 2
-// the value is max(z, 0) - |z| Q without a branch on the sign, and the slope
-// Phi + z phi takes the same exponential.  (|z| is capped in its product
-// with Q, whose value there is 0, so that an infinite z gives no NaN.)
-struct GeluParts {
-  float q, e;   // erfc(|z| / sqrt 2) / 2, exp(-z^2 / 2)
-};
-__device__ __forceinline__ GeluParts gelu_parts(float z) {
-  const float az = fabsf(z);
-  const float k = rcp_approx(fmaf(az, 0.3275911f * 0.70710678f, 1.f));
-  GeluParts r;
-  r.e = ex2_approx(z * z * (-0.5f * kLog2e));
-  float p = fmaf(k, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  p = fmaf(p, k, 0.5f * 1.421413741f);
-  p = fmaf(p, k, 0.5f * -0.284496736f);
-  p = fmaf(p, k, 0.5f * 0.254829592f);
-  r.q = p * k * r.e;
-  return r;
+// Forward values, two elements (or four) at a time: the epilogue's issue slots
+// and the 16 lanes of the special-function unit bound the products of few
+// channels, so the work goes to packed fp32 and as few special functions as
+// the accuracy allows.
+//
+// gelu(z) = z Phi(z) = max(z, 0) - t Q, t = |z|, Q = erfc(t / sqrt 2) / 2 =
+// e^(-t^2/2) R(t): one exponential, and R by a polynomial on [0, 6]
+// (fit_gelu_poly.py: |dQ| <= 0.081 (2^-12 Q + 1e-7), far below the result's
+// bf16 step; t is capped at 6 there and in its product with Q, whose value
+// beyond is below 1e-9).  The coefficients' signs are those of a polynomial
+// in -t.
+__device__ __forceinline__ uint64_t gelu_pair(uint64_t z) {
+  const float z0 = lo2(z), z1 = hi2(z);
+  const uint64_t nt = pk2(fmaxf(-fabsf(z0), -6.f), fmaxf(-fabsf(z1), -6.f));
+  const uint64_t arg = fmul2(fmul2(z, pk2(-0.5f * kLog2e, -0.5f * kLog2e)), z);
+  const uint64_t e = pk2(ex2_approx(lo2(arg)), ex2_approx(hi2(arg)));
+  uint64_t p = ffma2(nt, pk2(1.58075409e-06f, 1.58075409e-06f), pk2(4.28002786e-05f, 4.28002786e-05f));
+  p = ffma2(p, nt, pk2(0.000506665034f, 0.000506665034f));
+  p = ffma2(p, nt, pk2(0.00349101517f, 0.00349101517f));
+  p = ffma2(p, nt, pk2(0.0158246104f, 0.0158246104f));
+  p = ffma2(p, nt, pk2(0.0510843322f, 0.0510843322f));
+  p = ffma2(p, nt, pk2(0.125478402f, 0.125478402f));
+  p = ffma2(p, nt, pk2(0.247342557f, 0.247342557f));
+  p = ffma2(p, nt, pk2(0.398556024f, 0.398556024f));
+  p = ffma2(p, nt, pk2(0.499990076f, 0.499990076f));
+  return ffma2(fmul2(p, e), nt, pk2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
+}
+
+// silu(z) = z s, s = 1 / (1 + e^-z).  With E = e^-|z| <= 1 the logistic is
+// 1 / (1 + E) or E / (1 + E), exact in both tails, and the four reciprocals
+// come from one: 1/a = b c d / (a b c d), every factor within [1, 2].  (The
+// lower bound on the exponent keeps a NaN of one element out of the others;
+// its own comes back through the product with z.)
+__device__ __forceinline__ void silu_quad(uint64_t& z01, uint64_t& z23) {
+  const float z[4] = {lo2(z01), hi2(z01), lo2(z23), hi2(z23)};
+  float e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaxf(fabsf(z[i]) * -kLog2e, -150.f));
+  const uint64_t one = pk2(1.f, 1.f);
+  const uint64_t e01 = pk2(e[0], e[1]), e23 = pk2(e[2], e[3]);
+  const uint64_t a01 = fadd2(e01, one), a23 = fadd2(e23, one);
+  const float m01 = lo2(a01) * hi2(a01), m23 = lo2(a23) * hi2(a23);
+  const float r = rcp_approx(m01 * m23);
+  const float r01 = r * m23, r23 = r * m01;   // 1 / (a0 a1), 1 / (a2 a3)
+  const uint64_t s01 = fmul2(pk2(r01, r01), pk2(hi2(a01), lo2(a01)));
+  const uint64_t s23 = fmul2(pk2(r23, r23), pk2(hi2(a23), lo2(a23)));
+  const uint64_t f01 = fmul2(s01, e01), f23 = fmul2(s23, e23);
+  z01 = fmul2(z01, pk2(z[0] >= 0.f ? lo2(s01) : lo2(f01), z[1] >= 0.f ? hi2(s01) : hi2(f01)));
+  z23 = fmul2(z23, pk2(z[2] >= 0.f ? lo2(s23) : lo2(f23), z[3] >= 0.f ? hi2(s23) : hi2(f23)));
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
+__device__ __forceinline__ void act_quad(uint64_t& z01, uint64_t& z23) {
   if constexpr (ACT == kActGelu) {
-    const GeluParts g = gelu_parts(z);
-    return fmaf(-fminf(fabsf(z), 1e4f), g.q, fmaxf(z, 0.f));
+    z01 = gelu_pair(z01);
+    z23 = gelu_pair(z23);
   } else if constexpr (ACT == kActSilu) {
-    return z * rcp_approx(1.f + ex2_approx(-kLog2e * z));
-  } else {
-    return z;
+    silu_quad(z01, z23);
   }
 }
 
-// act(z) and act'(z)
+// act(z) and act'(z) for the backward, to fp32 accuracy (the bias gradients
+// are fp32 sums of what is formed from them).  gelu: with k = 1 / (1 + p t /
+// sqrt 2), Abramowitz and Stegun's formula 7.1.26 gives 2 Q = (a1 k + ... +
+// a5 k^5) e^(-t^2/2) to 1.5e-7; the slope is Phi + z phi, from the same
+// exponential.  (|z| is capped in products with Q and the exponential, whose
+// values there are 0, so that an infinite z gives no NaN.)
 template <int ACT>
 __device__ __forceinline__ void act_both(float z, float& a, float& da) {
   if constexpr (ACT == kActGelu) {
-    const GeluParts g = gelu_parts(z);
+    const float k = rcp_approx(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+    const float e = ex2_approx(z * z * (-0.5f * kLog2e));
+    float p = fmaf(k, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    p = fmaf(p, k, 0.5f * 1.421413741f);
+    p = fmaf(p, k, 0.5f * -0.284496736f);
+    p = fmaf(p, k, 0.5f * 0.254829592f);
+    const float q = p * k * e;
     const float cap = fminf(fmaxf(z, -1e4f), 1e4f);
-    a = fmaf(-fabsf(cap), g.q, fmaxf(z, 0.f));
-    da = fmaf(cap, 0.3989422804f * g.e, z > 0.f ? 1.f - g.q : g.q);
+    a = fmaf(-fabsf(cap), q, fmaxf(z, 0.f));
+    da = fmaf(cap, 0.3989422804f * e, z > 0.f ? 1.f - q : q);
   } else if constexpr (ACT == kActSilu) {
     const float s = rcp_approx(1.f + ex2_approx(-kLog2e * z));
     a = z * s;
@@ -115,17 +153,31 @@ __device__ __forceinline__ void act_both(float z, float& a, float& da) {
   }
 }
 
+// 16 columns' bias (fp32, from column `col` of n), zero outside or without one
+__device__ __forceinline__ void bias16(const float* bias, int col, int n, float4 (&b)[4]) {
+  if (bias && col + 16 <= n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = __ldg(reinterpret_cast<const float4*>(bias + col) + e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      b[e] = bias && col + 4 * e < n &&
+                     rib_guard(static_cast<size_t>(col) + 4 * e + 3, n, G_GEMM_BIAS)
+                 ? __ldg(reinterpret_cast<const float4*>(bias + col) + e)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
 // ---------------------------------------------------------------- the product
-constexpr int kGemmThreads = 320;
+constexpr int kGemmThreads = 576;
+constexpr int kGemmEpiWarps = 16, kGemmTmaWarp = 16, kGemmMmaWarp = 17;
 constexpr uint32_t kGemmATile = 128u * 128u;        // 128 rows x 64 channels
-constexpr uint32_t kGemmStage = 32u * 128u;         // one warp's staging: 32 rows x 64 columns
-constexpr uint32_t kGemmStaging = 8u * kGemmStage;
+constexpr uint32_t kGemmUnit = 32u * 64u;           // an epilogue unit: 32 rows x 32 bf16 columns
+constexpr uint32_t kGemmStaging = kGemmEpiWarps * kGemmUnit;
 constexpr int kGemmMaxStages = 10;
 
 struct GemmParams {
   const float* bias;               // [N], or [2][N] for kGated; may be null
-  const __nv_bfloat16* residual;   // [M][N]; may be null
-  int has_pre;                     // z is stored through tm_pre
   int M, N, K;
   int bn;                          // columns of a B tile in shared memory (64 .. 256)
   int m_tiles, n_tiles;
@@ -137,16 +189,16 @@ struct GemmParams {
 
 struct GemmBars {
   uint64_t full[kGemmMaxStages], empty[kGemmMaxStages];
-  uint64_t acc_full[2], acc_free[2], b_full, b_free, drain;
+  uint64_t acc_full[2], acc_free[2], b_full, b_free, drain, res[kGemmEpiWarps];
   uint32_t tmem;
   int abort_flag;
 };
 
 __host__ __device__ __forceinline__ size_t gemm_smem_bytes(int bn, int stages, int k_steps,
-                                                           bool resident) {
+                                                           bool resident, bool res) {
   const size_t b = static_cast<size_t>(bn) * 128;
   return 1024 + stages * (kGemmATile + (resident ? 0 : b)) + (resident ? k_steps * b : 0) +
-         kGemmStaging + sizeof(GemmBars);
+         (res ? 2 : 1) * kGemmStaging + sizeof(GemmBars);
 }
 
 // Columns of y that one tile gives: half of the B tile for kGated (the other
@@ -174,18 +226,19 @@ __device__ __forceinline__ void gemm_load_b(uint8_t* dst, const CUtensorMap* tm_
 // Items that run at the same time so share their x rows (one read from HBM
 // serves all column tiles), and a CTA keeps its column tile's weights.
 // grid min(items, SMs), block kGemmThreads, dynamic smem gemm_smem_bytes().
-template <int MODE, int ACT>
+template <int MODE, int ACT, bool RES, bool PRE>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_y,
-                const __grid_constant__ CUtensorMap tm_pre, const GemmParams p) {
+                const __grid_constant__ CUtensorMap tm_pre,
+                const __grid_constant__ CUtensorMap tm_res, const GemmParams p) {
   extern __shared__ uint8_t gemm_raw[];
   uint8_t* base = gemm_raw + ((1024u - (smem_u32(gemm_raw) & 1023u)) & 1023u);
   const uint32_t b_bytes = static_cast<uint32_t>(p.bn) * 128u;
   const uint32_t stage_bytes = kGemmATile + (p.b_resident ? 0u : b_bytes);
   uint8_t* s_res = base + p.stages * stage_bytes;
   uint8_t* s_stage = s_res + (p.b_resident ? p.k_steps * b_bytes : 0u);
-  GemmBars& bb = *reinterpret_cast<GemmBars*>(s_stage + kGemmStaging);
+  GemmBars& bb = *reinterpret_cast<GemmBars*>(s_stage + (RES ? 2 : 1) * kGemmStaging);
   volatile int* ab = &bb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tn = gemm_tile_cols<MODE>(p);
@@ -198,20 +251,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bb.acc_full[i], 1);
-      mbar_init(&bb.acc_free[i], 8);
+      mbar_init(&bb.acc_free[i], kGemmEpiWarps);
     }
     mbar_init(&bb.b_full, 1);
     mbar_init(&bb.b_free, 1);
     mbar_init(&bb.drain, 1);
+    for (int i = 0; i < kGemmEpiWarps; ++i) mbar_init(&bb.res[i], 1);
     bb.abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kGemmTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&tm_y);
   }
-  if (warp == 9) {
+  if (warp == kGemmMmaWarp) {
     tmem_alloc(&bb.tmem, 512);
     tmem_relinquish();
   }
@@ -220,7 +274,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bb.tmem;
 
-  if (warp == 8) {
+  if (warp == kGemmTmaWarp) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
@@ -258,7 +312,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           mbar_wait(&bb.full[i % p.stages], (i / p.stages) & 1, &no_abort, 200000000ull, SITE_GEMM);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kGemmMmaWarp) {
     // ---------------------------------------------------------- MMA issue
     const int last_steps = (p.K - 64 * (p.k_steps - 1) + 15) / 16;
     bool ok = true;
@@ -304,132 +358,144 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_GEMM);
   } else {
     // ---------------------------------------------------------- epilogue
-    // warp w: TMEM lane quarter w % 4 (tile rows 32 (w % 4) ..), every other
-    // 64-column chunk from w / 4.  A chunk goes through the warp's own 4 KB
-    // of shared memory (rows of 128 bytes, 128-byte swizzle) to one TMA store.
-    const int quarter = warp & 3, half = warp >> 2;
-    uint8_t* sg = s_stage + warp * kGemmStage;
+    // A tile's columns fall into units of 32; warp w takes TMEM lane quarter
+    // w % 4 (rows 32 (w % 4) .. of the tile) of the units that come to its group
+    // w / 4 as the groups take turns over all units of all tiles.  Sixteen
+    // warps of few registers, because a unit is a chain of latencies (tensor
+    // memory, special functions): four warps per scheduler fill each other's
+    // gaps.  Outputs leave through the warp's 2 KB of shared memory (rows of
+    // 64 bytes, 64-byte swizzle) and a TMA store, the residual comes in the
+    // same way, one unit ahead.
+    const int quarter = warp & 3, group = warp >> 2;
+    uint8_t* sg = s_stage + warp * kGemmUnit;
+    uint8_t* sr = sg + kGemmStaging;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const size_t res_n = static_cast<size_t>(p.M) * p.N;
+    // this lane's 16-byte granule g of its row
+    auto cell = [&](uint8_t* base, int g) {
+      return reinterpret_cast<uint4*>(base + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4));
+    };
     int t = 0;
-    bool ok = true;
+    int turn = 0;          // group whose turn the tile's first unit is
+    uint32_t res_ph = 0;   // parity of the next residual unit
+    bool ok = true, res_ahead = false;
+    auto load_res = [&](int m, int col) {   // one unit ahead; rows and columns outside are zeros
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bb.res[warp], kGemmUnit);
+        tma_load_2d(sr, &tm_res, &bb.res[warp], col, 128 * m + 32 * quarter);
+      }
+      res_ahead = true;
+    };
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
       const int n0 = (it % p.n_tiles) * tn;
-      const int cols = min(tn, p.N - n0), chunks = (cols + 63) / 64;
-      for (int m = it / p.n_tiles; m < p.m_tiles; m += p.splits, ++t) {
+      const int units = (min(tn, p.N - n0) + 31) / 32;
+      for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
         const int a = t & 1;
         const int row0 = 128 * m + 32 * quarter;
-        const bool row_in = row0 + lane < p.M;
+        const int first = (group - turn) & 3;
+        turn = (turn + units) & 3;
+        // the group's first unit of the next row tile of this item
+        const int next_m = m + p.splits, next_first = (group - turn) & 3;
+        if (RES && !res_ahead && first < units && row0 < p.M) load_res(m, n0 + 32 * first);
         if (!(ok = warp_wait(&bb.acc_full[a], (t >> 1) & 1, ab, lim, SITE_GEMM))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256 * a + lane_off;
-        for (int c = half; c < chunks; c += 2) {
-          uint32_t out[32], pre[MODE == kLinear ? 32 : 1];
+        for (int u = first; ok && u < units; u += 4) {
+          const int col = n0 + 32 * u;
+          uint32_t out[16];
+          [[maybe_unused]] uint32_t pre[PRE ? 16 : 1];
+          if constexpr (RES) {
+            if (row0 < p.M) {
+              if (!(ok = warp_wait(&bb.res[warp], res_ph, ab, lim, SITE_GEMM))) break;
+              res_ph ^= 1;
+              res_ahead = false;
+            }
+          }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = n0 + 64 * c + 32 * h;   // first of 32 columns
-            uint4 res[4];
+          for (int h = 0; h < 2; ++h) {   // 16 columns at a time
+            uint32_t v[16];
+            [[maybe_unused]] uint32_t w[16];
+            tmem_ld_x16(acc + 32 * u + 16 * h, v);
+            if constexpr (MODE == kGated) tmem_ld_x16(acc + tn + 32 * u + 16 * h, w);
+            [[maybe_unused]] float4 b[4], c[4];
+            if constexpr (MODE != kDx) bias16(p.bias, col + 16 * h, p.N, b);
+            if constexpr (MODE == kGated)
+              bias16(p.bias ? p.bias + p.N : nullptr, col + 16 * h, p.N, c);
+            tmem_wait_ld();
+            reg_fence_x16(v);
+            if constexpr (MODE == kGated) reg_fence_x16(w);
+            if (h == 1 && u + 4 >= units) {   // this warp has read its last columns
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bb.acc_free[a]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const size_t at = static_cast<size_t>(row0 + lane) * p.N + col + 8 * e;
-              res[e] = (MODE != kGated && p.residual && row_in && col + 8 * e < p.N &&
-                        rib_guard(at + 7, res_n, G_GEMM_RES))
-                           ? __ldg(reinterpret_cast<const uint4*>(p.residual + at))
-                           : make_uint4(0, 0, 0, 0);
-            }
-            uint32_t v[32];
-            tmem_ld_x32(acc + 64 * c + 32 * h, v);
-            if constexpr (MODE == kGated) {
-              uint32_t u[32];
-              tmem_ld_x32(acc + tn + 64 * c + 32 * h, u);
-              tmem_wait_ld();
-              reg_fence_x32(v);
-              reg_fence_x32(u);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float4 bg = make_float4(0.f, 0.f, 0.f, 0.f), bu = bg;
-                if (p.bias && col + 4 * e < p.N &&
-                    rib_guard(static_cast<size_t>(p.N) + col + 4 * e + 3, 2ull * p.N, G_GEMM_BIAS)) {
-                  bg = __ldg(reinterpret_cast<const float4*>(p.bias + col + 4 * e));
-                  bu = __ldg(reinterpret_cast<const float4*>(p.bias + p.N + col + 4 * e));
-                }
-                const float b4[4] = {bg.x, bg.y, bg.z, bg.w}, c4[4] = {bu.x, bu.y, bu.z, bu.w};
-                float y4[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y4[i] = act_value<ACT>(__uint_as_float(v[4 * e + i]) + b4[i]) *
-                          (__uint_as_float(u[4 * e + i]) + c4[i]);
-                out[16 * h + 2 * e] = pack_bf16x2(y4[0], y4[1]);
-                out[16 * h + 2 * e + 1] = pack_bf16x2(y4[2], y4[3]);
+              auto f = [](uint32_t x) { return __uint_as_float(x); };
+              uint64_t z01 = pk2(f(v[4 * e]), f(v[4 * e + 1]));
+              uint64_t z23 = pk2(f(v[4 * e + 2]), f(v[4 * e + 3]));
+              if constexpr (MODE != kDx) {
+                z01 = fadd2(z01, pk2(b[e].x, b[e].y));
+                z23 = fadd2(z23, pk2(b[e].z, b[e].w));
               }
-            } else {
-              tmem_wait_ld();
-              reg_fence_x32(v);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (MODE == kLinear && p.bias && col + 4 * e < p.N &&
-                    rib_guard(static_cast<size_t>(col) + 4 * e + 3, static_cast<size_t>(p.N),
-                              G_GEMM_BIAS))
-                  bv = __ldg(reinterpret_cast<const float4*>(p.bias + col + 4 * e));
-                const float z0 = __uint_as_float(v[4 * e]) + bv.x;
-                const float z1 = __uint_as_float(v[4 * e + 1]) + bv.y;
-                const float z2 = __uint_as_float(v[4 * e + 2]) + bv.z;
-                const float z3 = __uint_as_float(v[4 * e + 3]) + bv.w;
-                const uint32_t r01 = e & 1 ? res[e >> 1].z : res[e >> 1].x;
-                const uint32_t r23 = e & 1 ? res[e >> 1].w : res[e >> 1].y;
-                if constexpr (MODE == kLinear) {
-                  pre[16 * h + 2 * e] = pack_bf16x2(z0, z1);
-                  pre[16 * h + 2 * e + 1] = pack_bf16x2(z2, z3);
-                }
-                out[16 * h + 2 * e] =
-                    pack_bf16x2(act_value<ACT>(z0) + __uint_as_float(r01 << 16),
-                                act_value<ACT>(z1) + __uint_as_float(r01 & 0xffff0000u));
-                out[16 * h + 2 * e + 1] =
-                    pack_bf16x2(act_value<ACT>(z2) + __uint_as_float(r23 << 16),
-                                act_value<ACT>(z3) + __uint_as_float(r23 & 0xffff0000u));
+              if constexpr (PRE) {
+                pre[8 * h + 2 * e] = pack_bf16x2(lo2(z01), hi2(z01));
+                pre[8 * h + 2 * e + 1] = pack_bf16x2(lo2(z23), hi2(z23));
               }
+              act_quad<ACT>(z01, z23);
+              if constexpr (MODE == kGated) {
+                z01 = fmul2(z01, fadd2(pk2(f(w[4 * e]), f(w[4 * e + 1])), pk2(c[e].x, c[e].y)));
+                z23 = fmul2(z23, fadd2(pk2(f(w[4 * e + 2]), f(w[4 * e + 3])), pk2(c[e].z, c[e].w)));
+              }
+              if constexpr (RES) {
+                const uint2 r = *(reinterpret_cast<const uint2*>(cell(sr, 2 * h + (e >> 1))) + (e & 1));
+                z01 = fadd2(z01, pk2(f(r.x << 16), f(r.x & 0xffff0000u)));
+                z23 = fadd2(z23, pk2(f(r.y << 16), f(r.y & 0xffff0000u)));
+              }
+              out[8 * h + 2 * e] = pack_bf16x2(lo2(z01), hi2(z01));
+              out[8 * h + 2 * e + 1] = pack_bf16x2(lo2(z23), hi2(z23));
             }
           }
-          if (c + 2 >= chunks) {   // this warp has read its last columns
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bb.acc_free[a]);
-          }
-          auto put = [&](const uint32_t* w, const CUtensorMap* map) {
-            if (lane == 0) tma_store_wait_read_all();   // the last store has read the buffer
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              *reinterpret_cast<uint4*>(sg + lane * 128 + ((g ^ (lane & 7)) << 4)) =
-                  make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(map, sg, n0 + 64 * c, row0);
-              tma_store_commit();
-            }
-          };
           if (row0 < p.M) {
-            if constexpr (MODE == kLinear) {
-              if (p.has_pre) put(pre, &tm_pre);
-            }
+            auto put = [&](const uint32_t(&w)[16], const CUtensorMap* map) {
+              if (lane == 0) tma_store_wait_read_all();   // the last store has read the buffer
+              __syncwarp();
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                *cell(sg, g) = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(map, sg, col, row0);
+                tma_store_commit();
+              }
+            };
+            if constexpr (PRE) put(pre, &tm_pre);
             put(out, &tm_y);
+            if constexpr (RES) {   // every lane has read its residual (put's barriers)
+              if (u + 4 < units)
+                load_res(m, col + 128);
+              else if (next_m < p.m_tiles && next_first < units && 128 * next_m + 32 * quarter < p.M)
+                load_res(next_m, n0 + 32 * next_first);
+            }
           }
         }
-        if (half >= chunks) {   // no columns for this warp in a narrow tile
+        if (first >= units) {   // no unit of this tile for this warp
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bb.acc_free[a]);
         }
       }
     }
+    if (RES && !ok && res_ahead && lane == 0) {   // a residual load in flight lands first
+      volatile int no_abort = 0;
+      mbar_wait(&bb.res[warp], res_ph, &no_abort, 200000000ull, SITE_GEMM);
+    }
     // the stores are complete before the kernel's work is considered done
     if (lane == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kGemmMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -444,6 +510,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // one more column of the product: a block of ones stands behind x's channels
 // in each stage, so the sum of the bf16 dz is exact up to fp32 accumulation
 // and costs 16 of 208 MMA columns and no pass over dz.
+constexpr int kDwThreads = 320;
 constexpr int kDwStages = 3;
 constexpr int kDwBn = 192;
 constexpr uint32_t kDwAtom = 8192;                       // 64 rows x 64 channels
@@ -468,10 +535,10 @@ __host__ __device__ __forceinline__ size_t dw_smem_bytes() {
   return 1024 + kDwStages * kDwStageBytes + sizeof(DwBars);
 }
 
-// grid m_tiles * n_tiles * splits, block kGemmThreads, dynamic smem dw_smem_bytes().
+// grid m_tiles * n_tiles * splits, block kDwThreads, dynamic smem dw_smem_bytes().
 // tm_z: dz [rows][N], tm_x: x [rows][K], boxes of 64 channels x 64 rows,
 // 128-byte swizzle.
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kDwThreads, 1)
     dw_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_x,
               const DwParams p) {
   extern __shared__ uint8_t dwg_raw[];
@@ -499,7 +566,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (with_db) {
     // ones behind x's atoms (every element: the swizzle does not matter)
-    for (int i = threadIdx.x; i < kDwStages * 512; i += kGemmThreads)
+    for (int i = threadIdx.x; i < kDwStages * 512; i += kDwThreads)
       *reinterpret_cast<uint4*>(base + (i / 512) * kDwStageBytes + (4 + b_chunks) * kDwAtom +
                                 (i % 512) * 16) =
           make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);

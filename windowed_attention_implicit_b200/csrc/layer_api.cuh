@@ -56,30 +56,38 @@ struct GemmPlan {
   size_t smem;
 };
 
-GemmPlan plan_gemm(int M, int N, int K, bool gated, int sms) {
+GemmPlan plan_gemm(int M, int N, int K, bool gated, bool res, int sms) {
   GemmPlan g{};
   g.m_tiles = div_up(M, 128);
   g.k_steps = div_up(K, 64);
   const int unit = gated ? 128 : 64;             // bn is a multiple of this
   const int cols = gated ? 2 * N : N;
-  // the widest tiles that split the columns evenly, narrower ones while
-  // there are SMs without a tile
-  const int n = div_up(cols, 256);
-  g.bn = div_up(div_up(cols, n), unit) * unit;
-  while (g.bn > unit && (long long)g.m_tiles * div_up(cols, g.bn) < sms) g.bn -= unit;
-  g.n_tiles = div_up(cols, g.bn);
-  g.splits = pick_splits(g.m_tiles, g.n_tiles, sms);
+  // The tile width with the least work on the busiest CTA: tiles per CTA times
+  // a tile's cost, its columns plus about 48 for the x rows that every
+  // column tile reads again.
+  long long best = -1;
+  for (int bn = unit; bn <= 256; bn += unit) {
+    const int n_tiles = div_up(cols, bn), splits = pick_splits(g.m_tiles, n_tiles, sms);
+    const long long cost = (long long)div_up((long long)n_tiles * splits, sms) *
+                           div_up(g.m_tiles, splits) * (bn + 48);
+    if (best < 0 || cost < best) {
+      best = cost;
+      g.bn = bn;
+      g.n_tiles = n_tiles;
+      g.splits = splits;
+    }
+  }
   const int items = g.n_tiles * g.splits;
   g.grid = items < sms ? items : sms;
   const size_t b = (size_t)g.bn * 128;
-  const size_t room = kSmemMax - gemm_smem_bytes(0, 0, 0, false);
+  const size_t room = kSmemMax - gemm_smem_bytes(0, 0, 0, false, res);
   // weights stay in shared memory over an item's row tiles when at least
   // four stages of x still fit beside them
   g.resident = g.m_tiles >= 2 * g.splits && g.k_steps * b + 4 * kGemmATile <= room;
   const size_t left = room - (g.resident ? g.k_steps * b : 0);
   g.stages = static_cast<int>(left / (kGemmATile + (g.resident ? 0 : b)));
   if (g.stages > kGemmMaxStages) g.stages = kGemmMaxStages;
-  g.smem = gemm_smem_bytes(g.bn, g.stages, g.k_steps, g.resident);
+  g.smem = gemm_smem_bytes(g.bn, g.stages, g.k_steps, g.resident, res);
   return g;
 }
 
@@ -92,31 +100,49 @@ int map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint3
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, sw);
 }
 
-template <int MODE, int ACT>
-int launch_gemm(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
+template <int MODE, int ACT, bool RES, bool PRE>
+int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
                 const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
-  CUtensorMap ta, tb, ty, tp;
+  CUtensorMap ta, tb, ty, tp, tr;
   int rc = map_2d(&ta, a, M, K, 64, 128);
   if (!rc)
     rc = MODE == kLinear ? map_2d(&tb, b, N, K, 64, g.bn)
          : MODE == kGated ? map_2d(&tb, b, 2ull * N, K, 64, g.bn / 2)
                           : map_2d(&tb, b, K, N, 64, 64);
-  if (!rc) rc = map_2d(&ty, y, M, N, 64, 32);
-  if (!rc) rc = map_2d(&tp, pre ? pre : y, M, N, 64, 32);
+  if (!rc) rc = map_2d(&ty, y, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!rc) rc = map_2d(&tp, pre ? pre : y, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!rc)
+    rc = map_2d(&tr, residual ? residual : y, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc) return rc;
   GemmParams p{};
   p.bias = bias;
-  p.residual = static_cast<const __nv_bfloat16*>(residual);
-  p.has_pre = pre != nullptr;
   p.M = M; p.N = N; p.K = K;
   p.bn = g.bn;
   p.m_tiles = g.m_tiles; p.n_tiles = g.n_tiles; p.splits = g.splits;
   p.k_steps = g.k_steps; p.stages = g.stages; p.b_resident = g.resident;
   p.wait_limit_ns = g_wait_limit_ns;
-  if ((rc = set_smem(gemm_kernel<MODE, ACT>, g.smem))) return rc;
+  if ((rc = set_smem(gemm_kernel<MODE, ACT, RES, PRE>, g.smem))) return rc;
   TraceScope ts(kid, st);
-  gemm_kernel<MODE, ACT><<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, p);
+  gemm_kernel<MODE, ACT, RES, PRE><<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, tr, p);
   return launch_status();
+}
+
+// The epilogue's optional reads and writes are template arguments: an absent
+// one costs no instructions.
+template <int MODE, int ACT>
+int launch_gemm(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
+                const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
+#define RIB_GEMM(res, save) \
+  return launch_gemm_as<MODE, ACT, res, save>(kid, g, a, b, bias, residual, pre, y, M, N, K, st)
+  if constexpr (MODE == kLinear) {
+    if (residual && pre) RIB_GEMM(true, true);
+    if (pre) RIB_GEMM(false, true);
+  }
+  if constexpr (MODE != kGated) {
+    if (residual) RIB_GEMM(true, false);
+  }
+  RIB_GEMM(false, false);
+#undef RIB_GEMM
 }
 
 template <int MODE>
@@ -182,7 +208,7 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   if ((rc = set_smem(dw_kernel, smem))) return rc;
   {
     TraceScope ts(K_DW, st);
-    dw_kernel<<<d.m_tiles * d.n_tiles * d.splits, kGemmThreads, smem, st>>>(tz, tx, p);
+    dw_kernel<<<d.m_tiles * d.n_tiles * d.splits, kDwThreads, smem, st>>>(tz, tx, p);
     if ((rc = launch_status())) return rc;
   }
   {
@@ -211,66 +237,120 @@ bool aligned16_all(std::initializer_list<const void*> ptrs) {
 
 // ---------------------------------------------------------------- layer norm
 
-template <typename T>
-bool ln_vectors(const LnParams& p, int V) {
-  return p.C % V == 0 && aligned16_all({p.x, p.out, p.dy, p.dres});
-}
+// How one call runs: the asynchronous kernel's vector width, vectors per
+// lane, lanes per row and block, or (lanes == 0) a row kernel; and the grid,
+// which is also the number of dgamma / dbeta partials.
+struct LnPlan {
+  int vec, nv, lanes, grid;
+  LnBlocks q;
+  size_t smem;
+};
 
-int ln_grid_rows(int rows, bool cta, int per_warp, int sms, int per_sm) {
-  const long long want = cta ? rows : ((long long)rows + kLnWarps * per_warp - 1) /
-                                          (kLnWarps * per_warp);
-  const long long most = (long long)sms * per_sm;
-  return static_cast<int>(want < most ? want : most);
-}
-
-// Grid of the backward: two CTAs per SM (its registers allow two or three);
-// the CTAs' dgamma / dbeta partials are read back by the reduction, so more
-// CTAs than run at once would only lengthen it.
-int ln_bwd_grid(int rows, int C, int sms) {
-  return ln_grid_rows(rows, C > 1024, 1, sms, 2);
+LnPlan plan_ln(int rows, int C, int es, bool bwd, bool aligned, int sms) {
+  LnPlan n{};
+  const int arrays = bwd ? 3 : 1;   // also without dres: the sums then run in the same order
+  const int v = 16 / es;
+  n.vec = aligned && C % v == 0 ? v : 1;
+  if (aligned && C <= 1024) {
+    const int vecs = C / n.vec;
+    // as few lanes per row as keep four vectors a lane; single elements are
+    // dealt to the whole warp
+    n.lanes = n.vec == 1 ? 32 : vecs <= 16 ? 4 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
+    n.nv = div_up(vecs, n.lanes * (n.vec == 1 ? 2 : 1));
+    if (n.vec == 1 || n.nv > 4) n.nv = n.nv <= 4 ? 4 : n.nv <= 8 ? 8 : 16;
+    // A block: whole groups of rows, whole 16 bytes, 32 rows at most (a lane
+    // holds a row's statistics).  Measured at 192 channels of bf16: the forward
+    // is best at four rows (1.5 KB; 40.0 us for 294912 rows, 44 at sixteen), the
+    // backward at eight (3 KB of each array; 42 us with the sums for 147456
+    // rows, 56 at four: its fixed work per block is larger).
+    int unit = 32 / n.lanes;
+    while ((unit * C * es) % 16) unit *= 2;
+    n.q.rows = std::min(std::max(1, (bwd ? 9216 : 2048) / (arrays * unit * C * es)) * unit, 32);
+    n.q.bytes = (n.q.rows * C * es + 127) & ~127;
+    const size_t weights = ((bwd ? 1 : 2) * 4 * C + 127) & ~127;
+    for (n.q.stages = kLnMaxStages; n.q.stages >= 2; --n.q.stages) {
+      const size_t per_warp = (size_t)n.q.stages * arrays * n.q.bytes + kLnMaxStages * 8;
+      // two CTAs per SM where their stages fit
+      int ctas = 2, warps = (int)std::min<size_t>(bwd ? 12 : 16, (113 * 1024 - weights) / per_warp);
+      if (warps < 8) {
+        ctas = 1;
+        warps = (int)std::min<size_t>(bwd ? 12 : 16, (226 * 1024 - weights) / per_warp);
+      }
+      // at least six warps, and room for their dgamma / dbeta sums
+      if (warps < 6 || (bwd && per_warp < 8u * C)) continue;
+      // few rows: more, smaller CTAs finish sooner than few full ones
+      const int blocks = div_up(rows, n.q.rows);
+      n.q.warps = blocks < sms * warps ? div_up(blocks, sms) : warps;
+      n.smem = weights + n.q.warps * per_warp;
+      n.grid = std::min(sms * ctas, div_up(blocks, n.q.warps));
+      return n;
+    }
+  }
+  n.lanes = 0;
+  // a warp, or above 1024 channels a CTA, per row: a few CTAs per SM
+  const long long want = C > 1024 ? rows : div_up(rows, kLnWarps);
+  n.grid = static_cast<int>(std::min<long long>(want, sms * (bwd ? 2 : 8)));
+  return n;
 }
 
 template <typename T, int V, int NV, bool CTA>
-int ln_launch_fwd(const LnParams& p, int sms, cudaStream_t st) {
-  const int grid = ln_grid_rows(p.rows, CTA, ln_rows<V, NV, CTA>(), sms, 8);
-  TraceScope ts(K_LN_FWD, st);
-  layer_norm_fwd_kernel<T, V, NV, CTA><<<grid, kLnThreads, 0, st>>>(p);
-  return launch_status();
-}
-
-template <typename T, int V, int NV, bool CTA>
-int ln_launch_bwd(const LnParams& p, int sms, cudaStream_t st) {
+int ln_launch_row(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
+  if (!bwd) {
+    TraceScope ts(K_LN_FWD, st);
+    ln_row_fwd_kernel<T, V, NV, CTA><<<n.grid, kLnThreads, 0, st>>>(p);
+    return launch_status();
+  }
   const size_t smem = CTA || !p.part ? 0 : (size_t)kLnWarps * 2 * p.C * 4;
-  int rc = set_smem(layer_norm_bwd_kernel<T, V, NV, CTA>, smem);
+  int rc = set_smem(ln_row_bwd_kernel<T, V, NV, CTA>, smem);
   if (rc) return rc;
   TraceScope ts(K_LN_BWD, st);
-  layer_norm_bwd_kernel<T, V, NV, CTA>
-      <<<ln_bwd_grid(p.rows, p.C, sms), kLnThreads, smem, st>>>(p);
+  ln_row_bwd_kernel<T, V, NV, CTA><<<n.grid, kLnThreads, smem, st>>>(p);
   return launch_status();
 }
 
-// A row of up to 1024 channels belongs to a warp, a wider one to a CTA; rows
-// of whole 16-byte vectors at 16-byte addresses are read as such, others
-// element by element.
-template <typename T, bool FWD>
-int ln_dispatch(const LnParams& p, int sms, cudaStream_t st) {
+template <typename T, int V, int NV, int L>
+int ln_launch_async(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
+  auto kernel = bwd ? ln_async_kernel<T, V, NV, L, true> : ln_async_kernel<T, V, NV, L, false>;
+  int rc = set_smem(kernel, n.smem);
+  if (rc) return rc;
+  LnBlocks q = n.q;
+  q.wait_limit_ns = g_wait_limit_ns;
+  TraceScope ts(bwd ? K_LN_BWD : K_LN_FWD, st);
+  kernel<<<n.grid, 32 * q.warps, n.smem, st>>>(p, q);
+  return launch_status();
+}
+
+template <typename T>
+int ln_dispatch(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-#define RIB_LN(v, nv, cta)                                       \
-  return FWD ? ln_launch_fwd<T, v, nv, cta>(p, sms, st) \
-             : ln_launch_bwd<T, v, nv, cta>(p, sms, st)
-  const int C = p.C;
-  if (ln_vectors<T>(p, V)) {
-    if (C <= 32 * V) RIB_LN(V, 1, false);
-    if (C <= 64 * V) RIB_LN(V, 2, false);
-    if (C <= 1024) RIB_LN(V, 32 / V, false);
-    if (C <= 256 * V * 2) RIB_LN(V, 2, true);
-    RIB_LN(V, 32 / V, true);
+#define RIB_LN(V_, NV_, L_)                             \
+  if (n.vec == V_ && n.nv == NV_ && n.lanes == L_) \
+  return ln_launch_async<T, V_, NV_, L_>(p, n, bwd, st)
+  RIB_LN(V, 1, 4);
+  RIB_LN(V, 2, 4);
+  RIB_LN(V, 3, 4);
+  RIB_LN(V, 4, 4);
+  RIB_LN(V, 3, 8);
+  RIB_LN(V, 4, 8);
+  RIB_LN(V, 3, 16);
+  RIB_LN(V, 4, 16);
+  RIB_LN(V, 3, 32);
+  RIB_LN(V, 4, 32);
+  if constexpr (V == 4) {
+    RIB_LN(V, 8, 32);
   }
-  if (C <= 256) RIB_LN(1, 8, false);
-  if (C <= 1024) RIB_LN(1, 32, false);
-  if (C <= 2048) RIB_LN(1, 8, true);
-  RIB_LN(1, 32, true);
+  RIB_LN(1, 4, 32);
+  RIB_LN(1, 8, 32);
+  RIB_LN(1, 16, 32);
 #undef RIB_LN
+  const int C = p.C;
+  if (n.vec == V && C > 1024)
+    return C <= 256 * V * 2 ? ln_launch_row<T, V, 2, true>(p, n, bwd, st)
+                            : ln_launch_row<T, V, 32 / V, true>(p, n, bwd, st);
+  if (C <= 256) return ln_launch_row<T, 1, 8, false>(p, n, bwd, st);
+  if (C <= 1024) return ln_launch_row<T, 1, 32, false>(p, n, bwd, st);
+  if (C <= 2048) return ln_launch_row<T, 1, 8, true>(p, n, bwd, st);
+  return ln_launch_row<T, 1, 32, true>(p, n, bwd, st);
 }
 
 int ln_check(int dtype, int rows, int C) {
@@ -405,7 +485,7 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
   if (rc) return rc;
   if ((rc = set_smem(ffn_bwd_kernel<ACT>, w.f.smem))) return rc;
   TraceScope ts(K_FFN_BWD, st);
-  ffn_bwd_kernel<ACT><<<w.f.grid, kGemmThreads, w.f.smem, st>>>(tx, ty, ti, to, th, td, p);
+  ffn_bwd_kernel<ACT><<<w.f.grid, kFfnThreads, w.f.smem, st>>>(tx, ty, ti, to, th, td, p);
   return launch_status();
 }
 
@@ -432,14 +512,16 @@ int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* g
   p.x = x; p.out = y; p.gamma = gamma; p.beta = beta; p.mean = mean; p.rstd = rstd;
   p.rows = rows; p.C = C; p.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16, true>(p, sms, st)
-                                 : ln_dispatch<float, true>(p, sms, st);
+  const LnPlan n = plan_ln(rows, C, (int)es, false, aligned16_all({x, y}), sms);
+  return dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16>(p, n, false, st)
+                                 : ln_dispatch<float>(p, n, false, st);
 }
 
 size_t rib_layer_norm_bwd_workspace(int rows, int C) {
   int sms = 0;
   if (ln_check(RIB_DTYPE_BF16, rows, C) || rows == 0 || device_sms(&sms)) return 0;
-  return align256((size_t)ln_bwd_grid(rows, C, sms) * 2 * C * 4);
+  // at most two CTAs per SM leave partials, however the call runs
+  return align256((size_t)std::min(2 * sms, rows) * 2 * C * 4);
 }
 
 int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C,
@@ -471,12 +553,13 @@ int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C
   p.rstd = const_cast<float*>(rstd);
   p.part = sums ? static_cast<float*>(workspace) : nullptr;
   p.rows = rows; p.C = C;
-  rc = dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16, false>(p, sms, st)
-                               : ln_dispatch<float, false>(p, sms, st);
+  const LnPlan n = plan_ln(rows, C, (int)es, true, aligned16_all({x, dy, dres, dx}), sms);
+  rc = dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16>(p, n, true, st)
+                               : ln_dispatch<float>(p, n, true, st);
   if (rc || !sums) return rc;
   TraceScope ts(K_ROWS_RED, st);
-  reduce_rows_kernel<<<div_up(2 * C, 32), kLnThreads, 0, st>>>(p.part, ln_bwd_grid(rows, C, sms),
-                                                               C, dgamma, C, dbeta);
+  reduce_rows_kernel<<<div_up(2 * C, 32), kLnThreads, 0, st>>>(p.part, n.grid, C, dgamma, C,
+                                                               dbeta);
   return launch_status();
 }
 
@@ -489,7 +572,7 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
-  const GemmPlan g = plan_gemm(rows, N, K, false, sms);
+  const GemmPlan g = plan_gemm(rows, N, K, false, residual != nullptr, sms);
   return launch_gemm_act<kLinear>(act, K_LINEAR, g, x, w, bias, residual, pre, y, rows, N, K,
                                   static_cast<cudaStream_t>(stream));
 }
@@ -542,7 +625,7 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     }
   }
   if (dx) {
-    const GemmPlan g = plan_gemm(rows, K, N, false, sms);
+    const GemmPlan g = plan_gemm(rows, K, N, false, dx_add != nullptr, sms);
     rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, dz, w, nullptr, dx_add, nullptr, dx, rows, K,
                                     N, st);
     if (rc) return rc;
@@ -573,11 +656,11 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const GemmPlan g = plan_gemm(rows, hidden, C, true, sms);
+  const GemmPlan g = plan_gemm(rows, hidden, C, true, false, sms);
   rc = launch_gemm_act<kGated>(act, K_GATED, g, x, w_in, b_in, nullptr, nullptr, workspace, rows,
                                hidden, C, st);
   if (rc) return rc;
-  const GemmPlan o = plan_gemm(rows, C, hidden, false, sms);
+  const GemmPlan o = plan_gemm(rows, C, hidden, false, residual != nullptr, sms);
   return launch_gemm<kLinear, kActNone>(K_LINEAR, o, workspace, w_out, b_out, residual, nullptr, y,
                                         rows, C, hidden, st);
 }
@@ -630,7 +713,7 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
         p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr);
     if ((rc = launch_status())) return rc;
   }
-  const GemmPlan g = plan_gemm(rows, C, 2 * hidden, false, sms);
+  const GemmPlan g = plan_gemm(rows, C, 2 * hidden, false, dx_add != nullptr, sms);
   rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, ws + L.d, w_in, nullptr, dx_add, nullptr, dx,
                                   rows, C, 2 * hidden, st);
   if (rc) return rc;

@@ -5,16 +5,23 @@
 //   g = gamma dy,  dx = r (g - mean_c g - xh mean_c (g xh)) (+ dres)
 //   dgamma = sum_rows dy xh,  dbeta = sum_rows dy
 //
-// A row is read once: a group of threads (a warp, or a 256-thread CTA for
-// wide rows) holds it in registers as vectors of V elements, vector
-// t + threads * i in thread t, so every load of a warp is one contiguous run.
 // The variance is the mean of the squared deviations from the mean already
 // found (not E x^2 - mu^2, which cancels where |mu| is far above the spread).
 // Everything is fp32 between the load and the store; y and dx are rounded
-// once, to the features' type.
+// once, to the features' type.  Bound by HBM.
 //
-// Both kernels are bound by HBM: the grid is a few CTAs per SM that walk the
-// rows, each warp with kRows rows' loads in flight at once.
+// ln_async_kernel (up to 1024 channels): every warp runs its own pipeline over
+// blocks of a few rows.  Rows are contiguous, so a block is one run of bytes
+// whatever the channel count, odd ones included: a bulk copy brings it into
+// one of two or three shared-memory stages, the warp works on it there, writes y (or
+// dx) over x (or dy) and a bulk copy takes it back.  The next blocks are in
+// flight meanwhile, without holding registers, and no warp waits for another.  L lanes hold a row as vectors of V elements,
+// vector j + L i in lane j, so 192 channels of bf16 use all 32 lanes (four
+// rows of eight lanes, three vectors each) where a lane per vector would
+// idle a quarter of them.
+//
+// ln_row_*_kernel (wider rows, or pointers off a 16-byte address): a group of
+// threads (a CTA above 1024 channels, else a warp) holds a row in registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,14 +49,15 @@ struct LnParams {
   float eps;
 };
 
-// V consecutive elements as fp32
+// V consecutive elements as fp32 (plain loads, not the read-only path: y may
+// be x, and dx dy or dres)
 template <typename T, int V>
 struct LnVec;
 template <>
 struct LnVec<__nv_bfloat16, 8> {
   typedef uint4 raw;
   static __device__ __forceinline__ raw load(const void* p, size_t i) {
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
+    return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
   }
   static __device__ __forceinline__ raw zero() { return make_uint4(0, 0, 0, 0); }
   static __device__ __forceinline__ void get(const raw& r, float (&f)[8]) {
@@ -70,7 +78,7 @@ template <>
 struct LnVec<float, 4> {
   typedef float4 raw;
   static __device__ __forceinline__ raw load(const void* p, size_t i) {
-    return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
   }
   static __device__ __forceinline__ raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
   static __device__ __forceinline__ void get(const raw& r, float (&f)[4]) {
@@ -147,7 +155,7 @@ __host__ __device__ constexpr int ln_rows() {
 // -------------------------------------------------------------- forward
 // grid: a few CTAs per SM (ln_grid), block kLnThreads.
 template <typename T, int V, int NV, bool CTA>
-__global__ void __launch_bounds__(kLnThreads) layer_norm_fwd_kernel(const LnParams p) {
+__global__ void __launch_bounds__(kLnThreads) ln_row_fwd_kernel(const LnParams p) {
   using L = LnVec<T, V>;
   constexpr int R = ln_rows<V, NV, CTA>();
   constexpr int G = CTA ? kLnThreads : 32;
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_fwd_kernel(const LnPara
 // Dynamic shared memory: kLnWarps * 2 * C floats for warp groups when the
 // sums are wanted, else none.
 template <typename T, int V, int NV, bool CTA>
-__global__ void __launch_bounds__(kLnThreads) layer_norm_bwd_kernel(const LnParams p) {
+__global__ void __launch_bounds__(kLnThreads) ln_row_bwd_kernel(const LnParams p) {
   using L = LnVec<T, V>;
   constexpr int R = V * NV <= 8 && !CTA ? 2 : 1;
   constexpr int G = CTA ? kLnThreads : 32;
@@ -394,6 +402,419 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_bwd_kernel(const LnPara
 #pragma unroll
       for (int k = 0; k < kLnWarps; ++k) s += ln_sums[static_cast<size_t>(k) * 2 * C + c];
       if (rib_guard(part_0 + c, part_n, G_LN_PART)) mine[c] = s;
+    }
+  }
+}
+
+// -------------------------------------------------------------- blocks of rows
+constexpr int kLnMaxStages = 3;
+constexpr int SITE_LN = 45;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait_read_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+struct LnBlocks {
+  int rows;              // rows of a block
+  uint32_t bytes;        // its bytes in shared memory (a multiple of 128)
+  int warps;             // per CTA
+  int stages;            // 2 or 3
+  uint64_t wait_limit_ns;
+};
+
+// Slot i of a lane: what it holds of a row at a time, as P packed fp32 pairs,
+// to and from shared memory.  Whole vectors: vector j + L i (V elements, V / 2
+// pairs).  Single elements (V = 1, L = 32): elements j + 64 i and j + 64 i + 32
+// as one pair.  `row` is the row's first byte; elements beyond C read as zero
+// and are not written (a vector beyond C is not asked for).
+template <typename T, int V, int L>
+struct LnSlot;
+template <int L>
+struct LnSlot<__nv_bfloat16, 8, L> {
+  static constexpr int P = 4;
+  static __device__ __forceinline__ void get(const uint8_t* row, int i, int j, int, uint64_t (&f)[4]) {
+    const uint4 r = *reinterpret_cast<const uint4*>(row + 16 * (j + L * i));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = pk2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void put(uint8_t* row, int i, int j, int, const uint64_t (&f)[4]) {
+    *reinterpret_cast<uint4*>(row + 16 * (j + L * i)) =
+        make_uint4(pack_bf16x2(lo2(f[0]), hi2(f[0])), pack_bf16x2(lo2(f[1]), hi2(f[1])),
+                   pack_bf16x2(lo2(f[2]), hi2(f[2])), pack_bf16x2(lo2(f[3]), hi2(f[3])));
+  }
+};
+template <int L>
+struct LnSlot<float, 4, L> {
+  static constexpr int P = 2;
+  static __device__ __forceinline__ void get(const uint8_t* row, int i, int j, int, uint64_t (&f)[2]) {
+    const float4 r = *reinterpret_cast<const float4*>(row + 16 * (j + L * i));
+    f[0] = pk2(r.x, r.y);
+    f[1] = pk2(r.z, r.w);
+  }
+  static __device__ __forceinline__ void put(uint8_t* row, int i, int j, int, const uint64_t (&f)[2]) {
+    *reinterpret_cast<float4*>(row + 16 * (j + L * i)) =
+        make_float4(lo2(f[0]), hi2(f[0]), lo2(f[1]), hi2(f[1]));
+  }
+};
+template <typename T>
+struct LnSlot<T, 1, 32> {
+  static constexpr int P = 1;
+  static __device__ __forceinline__ void get(const uint8_t* row, int i, int j, int C, uint64_t (&f)[1]) {
+    const T* r = reinterpret_cast<const T*>(row);
+    const int c = j + 64 * i;
+    f[0] = pk2(c < C ? static_cast<float>(r[c]) : 0.f, c + 32 < C ? static_cast<float>(r[c + 32]) : 0.f);
+  }
+  static __device__ __forceinline__ void put(uint8_t* row, int i, int j, int C, const uint64_t (&f)[1]) {
+    T* r = reinterpret_cast<T*>(row);
+    const int c = j + 64 * i;
+    if (c < C) r[c] = static_cast<T>(lo2(f[0]));   // to nearest
+    if (c + 32 < C) r[c + 32] = static_cast<T>(hi2(f[0]));
+  }
+};
+// column of half h of pair e of slot i
+template <int V, int L>
+__device__ __forceinline__ int ln_column(int i, int j, int e, int h) {
+  return V == 1 ? j + 64 * i + 32 * h : (j + L * i) * V + 2 * e + h;
+}
+
+template <int L>
+__device__ __forceinline__ float ln_lane_sum(float v) {
+#pragma unroll
+  for (int m = L / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+__device__ __forceinline__ float ln_pair_sum(uint64_t v) { return lo2(v) + hi2(v); }
+__device__ __forceinline__ uint64_t ln_both(float v) { return pk2(v, v); }
+
+// gamma or beta of vector `vec` from shared memory.  The vectors' first four
+// floats lie together and their last four behind all of those, so that
+// neighbouring lanes read neighbouring 16 bytes.
+template <int V>
+__device__ __forceinline__ int ln_weight_slot(int c, int C) {
+  return V == 8 ? (c & 4 ? C / 2 : 0) + (c >> 3) * 4 + (c & 3) : c;
+}
+template <int V, int L, int P>
+__device__ __forceinline__ void ln_weight_get(const float* w, int i, int j, int C, uint64_t (&f)[P]) {
+  if constexpr (V == 1) {
+    const int c = j + 64 * i;
+    f[0] = pk2(c < C ? w[c] : 0.f, c + 32 < C ? w[c + 32] : 0.f);
+  } else {
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const float4 r = *reinterpret_cast<const float4*>(w + h * (C / 2) + 4 * (j + L * i));
+      f[2 * h] = pk2(r.x, r.y);
+      f[2 * h + 1] = pk2(r.z, r.w);
+    }
+  }
+}
+
+// grid: CTAs that fit the SMs; block 32 * q.warps; dynamic shared memory:
+// gamma (and beta) [C] fp32, then each warp's stages, then its barriers.  At
+// the end of the backward the stages hold the warps' sums.
+template <typename T, int V, int NV, int L, bool BWD>
+__global__ void __launch_bounds__(BWD ? 384 : 512)
+    ln_async_kernel(const LnParams p, const LnBlocks q) {
+  using LP = LnSlot<T, V, L>;
+  constexpr int P = LP::P;
+  constexpr int G = 32 / L;   // rows side by side
+  // rows whose chains of shuffles run interleaved, where the registers allow
+  constexpr int RR = L == 32 && NV * P <= 8 ? 2 : 1;
+  constexpr uint32_t ES = sizeof(T);
+  extern __shared__ __align__(128) uint8_t ln_smem[];
+  __shared__ int abort_flag;
+  volatile int* ab = &abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = lane & (L - 1), grp = lane / L;
+  const int C = p.C, arrays = BWD ? (p.dres ? 3 : 2) : 1;
+  const uint32_t w_bytes = (static_cast<uint32_t>(BWD ? 1 : 2) * 4 * C + 127u) & ~127u;
+  const uint32_t warp_bytes = q.stages * arrays * q.bytes;
+  float* s_gamma = reinterpret_cast<float*>(ln_smem);
+  float* s_beta = s_gamma + C;
+  uint8_t* mine = ln_smem + w_bytes + warp * warp_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ln_smem + w_bytes + q.warps * warp_bytes) +
+                   warp * kLnMaxStages;
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < q.stages; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+  }
+  for (int c = threadIdx.x; c < C; c += blockDim.x) {
+    s_gamma[ln_weight_slot<V>(c, C)] = p.gamma ? __ldg(p.gamma + c) : 1.f;
+    if (!BWD) s_beta[ln_weight_slot<V>(c, C)] = p.beta ? __ldg(p.beta + c) : 0.f;
+  }
+  __syncthreads();
+  const float inv_c = 1.f / static_cast<float>(C);
+  const uint32_t row_bytes = C * ES;
+  const int blocks = (p.rows + q.rows - 1) / q.rows;
+  const int step = gridDim.x * q.warps, first = warp * gridDim.x + blockIdx.x;
+  const uint8_t* src[3] = {static_cast<const uint8_t*>(p.x), static_cast<const uint8_t*>(p.dy),
+                           static_cast<const uint8_t*>(p.dres)};
+  uint8_t* out = static_cast<uint8_t*>(p.out);
+  const size_t all_bytes = static_cast<size_t>(p.rows) * row_bytes;
+  auto rows_of = [&](int b) { return min(q.rows, p.rows - b * q.rows); };
+  auto at = [&](int b) { return static_cast<size_t>(b) * (q.rows * row_bytes); };
+  auto stage = [&](int s, int a) { return mine + (s * arrays + a) * q.bytes; };
+  // Starts block b's copies into stage s; the up to 15 bytes behind its last
+  // whole 16 (a last block of rows of an odd size only) are copied by the lanes.
+  auto load = [&](int b, int s) {
+    const uint32_t bytes = rows_of(b) * row_bytes, whole = V == 1 ? bytes & ~15u : bytes;
+    if (V == 1 && bytes != whole) {
+      for (int a = 0; a < arrays; ++a)
+        if (lane < (bytes - whole) / ES &&
+            rib_guard(at(b) + whole + lane * ES, all_bytes, G_LN_IN))
+          reinterpret_cast<T*>(stage(s, a) + whole)[lane] =
+              reinterpret_cast<const T*>(src[a] + at(b) + whole)[lane];
+      __syncwarp();
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[s], arrays * whole);
+      for (int a = 0; a < arrays && whole; ++a)
+        bulk_load(stage(s, a), src[a] + at(b), whole, &full[s]);
+    }
+  };
+  // the rows' statistics, lane r holding row r of the next block
+  float mu_next = 0.f, rs_next = 0.f;
+  auto load_stats = [&](int b) {
+    if (BWD && b < blocks && lane < rows_of(b)) {
+      const size_t r = static_cast<size_t>(b) * q.rows + lane;
+      if (rib_guard(r, p.rows, G_LN_STAT)) {
+        mu_next = __ldg(p.mean + r);
+        rs_next = __ldg(p.rstd + r);
+      }
+    }
+  };
+  [[maybe_unused]] uint64_t sg[BWD ? NV : 1][P], sb[BWD ? NV : 1][P];
+  if constexpr (BWD) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < P; ++e) sg[i][e] = sb[i][e] = 0ull;
+  }
+  bool ok = true;
+  int loaded = 0, ahead = first;   // blocks whose copies were started; the next one
+  for (; loaded < q.stages - 1 && ahead < blocks; ahead += step, ++loaded) load(ahead, loaded);
+  load_stats(first);
+  int s = 0, s_load = q.stages - 1;
+  uint32_t ph = 0;
+  int n = 0;
+  for (int b = first; b < blocks; b += step, ++n) {
+    const float mu_b = mu_next, rs_b = rs_next;
+    load_stats(b + step);
+    if (!(ok = warp_wait(&full[s], ph, ab, q.wait_limit_ns, SITE_LN))) break;
+    const int rows = rows_of(b);
+    uint8_t* x0 = stage(s, 0);
+    for (int r0 = 0; r0 < rows; r0 += G * RR) {
+      uint32_t off[RR];
+      bool in_row[RR];
+#pragma unroll
+      for (int k = 0; k < RR; ++k) {
+        in_row[k] = r0 + grp + G * k < rows;
+        off[k] = (r0 + grp + G * k) * row_bytes;
+      }
+      if constexpr (!BWD) {
+        uint64_t f[RR][NV][P];
+        float mu[RR], rs[RR];
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          uint64_t sum = 0ull;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (in_row[k] && ln_column<V, L>(i, j, 0, 0) < C) {
+              LP::get(x0 + off[k], i, j, C, f[k][i]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < P; ++e) f[k][i][e] = 0ull;
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) sum = fadd2(sum, f[k][i][e]);
+          }
+          mu[k] = ln_pair_sum(sum);
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) mu[k] = ln_lane_sum<L>(mu[k]) * inv_c;
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          uint64_t sq = 0ull;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (ln_column<V, L>(i, j, 0, 0) >= C) continue;
+            // an element beyond C stays zero
+            const uint64_t neg =
+                pk2(-mu[k], V == 1 && ln_column<V, L>(i, j, 0, 1) >= C ? 0.f : -mu[k]);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              f[k][i][e] = fadd2(f[k][i][e], neg);
+              sq = ffma2(f[k][i][e], f[k][i][e], sq);
+            }
+          }
+          rs[k] = ln_pair_sum(sq);
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) rs[k] = rsqrtf(ln_lane_sum<L>(rs[k]) * inv_c + p.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (ln_column<V, L>(i, j, 0, 0) >= C) continue;
+          uint64_t g[P], bt[P];
+          ln_weight_get<V, L>(s_gamma, i, j, C, g);
+          ln_weight_get<V, L>(s_beta, i, j, C, bt);
+#pragma unroll
+          for (int k = 0; k < RR; ++k) {
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+              f[k][i][e] = ffma2(fmul2(f[k][i][e], ln_both(rs[k])), g[e], bt[e]);
+            if (in_row[k]) LP::put(x0 + off[k], i, j, C, f[k][i]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          const size_t row = static_cast<size_t>(b) * q.rows + r0 + grp + G * k;
+          if (j == 0 && in_row[k] && rib_guard(row, p.rows, G_LN_STAT)) {
+            if (p.mean) p.mean[row] = mu[k];
+            if (p.rstd) p.rstd[row] = rs[k];
+          }
+        }
+      } else {
+        uint8_t* d0 = stage(s, 1);
+        float mu[RR], rs[RR], m1[RR], m2[RR];
+        uint64_t xc[RR][NV][P], gd[RR][NV][P];   // x - mean, gamma dy
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          mu[k] = __shfl_sync(0xffffffffu, mu_b, (r0 + grp + G * k) & 31);
+          rs[k] = __shfl_sync(0xffffffffu, rs_b, (r0 + grp + G * k) & 31);
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          uint64_t s1 = 0ull, s2 = 0ull;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (!in_row[k] || ln_column<V, L>(i, j, 0, 0) >= C) continue;
+            uint64_t d[P], g[P];
+            LP::get(x0 + off[k], i, j, C, xc[k][i]);
+            LP::get(d0 + off[k], i, j, C, d);   // zero beyond C, so its terms vanish
+            ln_weight_get<V, L>(s_gamma, i, j, C, g);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              xc[k][i][e] = fadd2(xc[k][i][e], ln_both(-mu[k]));
+              gd[k][i][e] = fmul2(d[e], g[e]);
+              const uint64_t xh = fmul2(xc[k][i][e], ln_both(rs[k]));
+              sg[i][e] = ffma2(d[e], xh, sg[i][e]);
+              sb[i][e] = fadd2(sb[i][e], d[e]);
+              s1 = fadd2(s1, gd[k][i][e]);
+              s2 = ffma2(gd[k][i][e], xh, s2);
+            }
+          }
+          m1[k] = ln_pair_sum(s1);
+          m2[k] = ln_pair_sum(s2);
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          m1[k] = ln_lane_sum<L>(m1[k]) * inv_c;
+          m2[k] = ln_lane_sum<L>(m2[k]) * inv_c;
+        }
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          // dx = r g + (-r^2 m2) (x - mean) + (dres - r m1)
+          const uint64_t kg = ln_both(rs[k]), kx = ln_both(-rs[k] * rs[k] * m2[k]),
+                         k1 = ln_both(-rs[k] * m1[k]);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (!in_row[k] || ln_column<V, L>(i, j, 0, 0) >= C) continue;
+            uint64_t a[P];
+            if (arrays == 3) {
+              LP::get(stage(s, 2) + off[k], i, j, C, a);
+            } else {
+#pragma unroll
+              for (int e = 0; e < P; ++e) a[e] = 0ull;
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+              a[e] = ffma2(kg, gd[k][i][e], ffma2(kx, xc[k][i][e], fadd2(a[e], k1)));
+            LP::put(d0 + off[k], i, j, C, a);
+          }
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    {
+      const uint8_t* res = stage(s, BWD ? 1 : 0);
+      const uint32_t bytes = rows * row_bytes, whole = V == 1 ? bytes & ~15u : bytes;
+      if (V == 1 && lane < (bytes - whole) / ES &&
+          rib_guard(at(b) + whole + lane * ES, all_bytes, G_LN_OUT))
+        reinterpret_cast<T*>(out + at(b) + whole)[lane] =
+            reinterpret_cast<const T*>(res + whole)[lane];
+      if (lane == 0) {
+        if (whole) bulk_store(out + at(b), res, whole);
+        tma_store_commit();
+        // the stage that the next copies go to (the block before this one's,
+        // or with two stages the one before that) has been read
+        bulk_store_wait_read_one();
+      }
+      __syncwarp();
+    }
+    if (ahead < blocks) {
+      load(ahead, s_load);
+      ++loaded;
+      ahead += step;
+      if (++s_load == q.stages) s_load = 0;
+    }
+    if (++s == q.stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  if (!ok && lane == 0) {   // copies in flight land before the CTA exits
+    volatile int no_abort = 0;
+    for (int i = n; i < loaded; ++i)
+      mbar_wait(&full[i % q.stages], (i / q.stages) & 1, &no_abort, 200000000ull, SITE_LN);
+  }
+  if (lane == 0) tma_store_wait_all();
+  if constexpr (BWD) {
+    if (!p.part) return;
+    // sum over the rows' lane groups, then over the warps in order
+    __syncthreads();   // every warp is done with its stages
+    float* sums = reinterpret_cast<float*>(ln_smem + w_bytes);   // [warps][2][C]
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float g = h ? hi2(sg[i][e]) : lo2(sg[i][e]), t = h ? hi2(sb[i][e]) : lo2(sb[i][e]);
+#pragma unroll
+          for (int m = L; m < 32; m <<= 1) {
+            g += __shfl_xor_sync(0xffffffffu, g, m);
+            t += __shfl_xor_sync(0xffffffffu, t, m);
+          }
+          const int c = ln_column<V, L>(i, j, e, h);
+          if (grp == 0 && c < C) {
+            sums[(2 * warp) * C + c] = g;
+            sums[(2 * warp + 1) * C + c] = t;
+          }
+        }
+      }
+    __syncthreads();
+    const size_t part_0 = static_cast<size_t>(blockIdx.x) * 2 * C;
+    for (int c = threadIdx.x; c < 2 * C; c += blockDim.x) {
+      float v = 0.f;
+      for (int w = 0; w < q.warps; ++w) v += sums[2 * w * C + c];
+      if (rib_guard(part_0 + c, static_cast<size_t>(gridDim.x) * 2 * C, G_LN_PART))
+        p.part[part_0 + c] = v;
     }
   }
 }
