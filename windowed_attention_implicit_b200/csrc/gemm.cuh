@@ -54,6 +54,90 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// Two CTAs of a cluster work as one 256-row tile (cta_group::2): each holds
+// its 128 rows of A and of the accumulator and half of B; CTA 0 issues the
+// MMAs, which read both shared memories.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of CTA `rank`'s copy of a shared variable, for remote arrivals.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+// (CTA scope: what it orders are tensor-memory reads, which the tcgen05 fence
+// before it and the one after the wait order; a cluster-scope release also
+// waits for all earlier stores, about 2400 cycles.)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// A load into this CTA's shared memory that reports to `bar`, a barrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(dst)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 1)
+    tmem_dealloc(addr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void pair_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  if constexpr (CG == 1)
+    umma_ss_elect(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    umma_commit_elect(bar);
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], m;\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
 // ---------------------------------------------------------------- activations
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -91,27 +175,34 @@ __device__ __forceinline__ uint64_t gelu_pair(uint64_t z) {
   return ffma2(fmul2(p, e), nt, pk2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
 }
 
-// silu(z) = z s, s = 1 / (1 + e^-z).  With E = e^-|z| <= 1 the logistic is
-// 1 / (1 + E) or E / (1 + E), exact in both tails, and the four reciprocals
-// come from one: 1/a = b c d / (a b c d), every factor within [1, 2].  (The
-// lower bound on the exponent keeps a NaN of one element out of the others;
-// its own comes back through the product with z.)
+// silu(z) = z / (1 + e^-z) = max(z, 0) - |z| f with E = e^-|z| <= 1 and f = E / (1
+// + E), exact in both tails; the four reciprocals come from one: 1/a = b c d /
+// (a b c d), every factor within [1, 2].  (-|z| is bounded so that a NaN of one
+// element stays out of the others; its own comes back through the maximum,
+// which keeps it.)
+__device__ __forceinline__ float max0_nan(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void silu_quad(uint64_t& z01, uint64_t& z23) {
   const float z[4] = {lo2(z01), hi2(z01), lo2(z23), hi2(z23)};
-  float e[4];
+  float m[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaxf(fabsf(z[i]) * -kLog2e, -150.f));
-  const uint64_t one = pk2(1.f, 1.f);
-  const uint64_t e01 = pk2(e[0], e[1]), e23 = pk2(e[2], e[3]);
-  const uint64_t a01 = fadd2(e01, one), a23 = fadd2(e23, one);
-  const float m01 = lo2(a01) * hi2(a01), m23 = lo2(a23) * hi2(a23);
-  const float r = rcp_approx(m01 * m23);
-  const float r01 = r * m23, r23 = r * m01;   // 1 / (a0 a1), 1 / (a2 a3)
-  const uint64_t s01 = fmul2(pk2(r01, r01), pk2(hi2(a01), lo2(a01)));
-  const uint64_t s23 = fmul2(pk2(r23, r23), pk2(hi2(a23), lo2(a23)));
-  const uint64_t f01 = fmul2(s01, e01), f23 = fmul2(s23, e23);
-  z01 = fmul2(z01, pk2(z[0] >= 0.f ? lo2(s01) : lo2(f01), z[1] >= 0.f ? hi2(s01) : hi2(f01)));
-  z23 = fmul2(z23, pk2(z[2] >= 0.f ? lo2(s23) : lo2(f23), z[3] >= 0.f ? hi2(s23) : hi2(f23)));
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(-fabsf(z[i]), -103.f);
+  const uint64_t k = pk2(kLog2e, kLog2e), one = pk2(1.f, 1.f);
+  const uint64_t m01 = pk2(m[0], m[1]), m23 = pk2(m[2], m[3]);
+  const uint64_t x01 = fmul2(m01, k), x23 = fmul2(m23, k);
+  const float e0 = ex2_approx(lo2(x01)), e1 = ex2_approx(hi2(x01));
+  const float e2 = ex2_approx(lo2(x23)), e3 = ex2_approx(hi2(x23));
+  const uint64_t a01 = fadd2(pk2(e0, e1), one), a23 = fadd2(pk2(e2, e3), one);
+  const float p01 = lo2(a01) * hi2(a01), p23 = lo2(a23) * hi2(a23);
+  const float r = rcp_approx(p01 * p23);
+  const float r01 = r * p23, r23 = r * p01;   // 1 / (a0 a1), 1 / (a2 a3)
+  const uint64_t f01 = fmul2(pk2(e0 * hi2(a01), e1 * lo2(a01)), pk2(r01, r01));
+  const uint64_t f23 = fmul2(pk2(e2 * hi2(a23), e3 * lo2(a23)), pk2(r23, r23));
+  z01 = ffma2(m01, f01, pk2(max0_nan(z[0]), max0_nan(z[1])));
+  z23 = ffma2(m23, f23, pk2(max0_nan(z[2]), max0_nan(z[3])));
 }
 
 template <int ACT>
@@ -194,10 +285,17 @@ struct GemmBars {
   int abort_flag;
 };
 
-__host__ __device__ __forceinline__ size_t gemm_smem_bytes(int bn, int stages, int k_steps,
-                                                           bool resident, bool res) {
-  const size_t b = static_cast<size_t>(bn) * 128;
-  return 1024 + stages * (kGemmATile + (resident ? 0 : b)) + (resident ? k_steps * b : 0) +
+// Bytes of one k-step of B in one CTA: bn columns, or half of them in a pair
+// (whole 64-column atoms where the columns are the leading dimension).
+__host__ __device__ __forceinline__ uint32_t gemm_b_bytes(int mode, int cg, int bn) {
+  const int cols = cg == 1 ? bn : mode == kDx ? (bn / 2 + 63) / 64 * 64 : bn / 2;
+  return static_cast<uint32_t>(cols) * 128u;
+}
+
+__host__ __device__ __forceinline__ size_t gemm_smem_bytes(uint32_t b_bytes, int stages,
+                                                           int k_steps, bool resident, bool res) {
+  return 1024 + static_cast<size_t>(stages) * (kGemmATile + (resident ? 0 : b_bytes)) +
+         (resident ? static_cast<size_t>(k_steps) * b_bytes : 0) +
          (res ? 2 : 1) * kGemmStaging + sizeof(GemmBars);
 }
 
@@ -208,25 +306,54 @@ __device__ __forceinline__ int gemm_tile_cols(const GemmParams& p) {
   return MODE == kGated ? p.bn / 2 : p.bn;
 }
 
-// Loads the B tile of column tile n, k-step k (64 deep) to `dst`.
-template <int MODE>
+// MMA columns of the column tile at n0: a last tile narrower than bn takes a
+// narrower MMA (16 columns per CTA at a time).
+template <int MODE, int CG>
+__device__ __forceinline__ int gemm_mma_cols(const GemmParams& p, int n0) {
+  constexpr int unit = 16 * CG;
+  return MODE == kGated ? p.bn : min(p.bn, (p.N - n0 + unit - 1) / unit * unit);
+}
+
+// Loads this CTA's share of the B tile at column n0, k-step k (64 deep), to
+// `dst`; `bar` is the barrier that counts it.
+template <int MODE, int CG>
 __device__ __forceinline__ void gemm_load_b(uint8_t* dst, const CUtensorMap* tm_b, uint64_t* bar,
-                                            const GemmParams& p, int n0, int k) {
-  if constexpr (MODE == kLinear) {
-    tma_load_2d(dst, tm_b, bar, 64 * k, n0);
-  } else if constexpr (MODE == kGated) {
-    tma_load_2d(dst, tm_b, bar, 64 * k, n0);
-    tma_load_2d(dst + p.bn * 64, tm_b, bar, 64 * k, p.N + n0);
+                                            uint32_t pair_bar, const GemmParams& p, int n0, int k,
+                                            uint32_t rank) {
+  auto load = [&](uint8_t* d, int c0, int c1) {
+    if constexpr (CG == 1)
+      tma_load_2d(d, tm_b, bar, c0, c1);
+    else
+      tma_load_2d_pair(d, tm_b, pair_bar, c0, c1);
+  };
+  if constexpr (MODE == kGated) {
+    if constexpr (CG == 1) {
+      load(dst, 64 * k, n0);
+      load(dst + p.bn * 64, 64 * k, p.N + n0);
+    } else {   // CTA 0 holds the gate's rows, CTA 1 the other projection's
+      load(dst, 64 * k, rank * p.N + n0);
+    }
   } else {
-    for (int c = 0; c < p.bn / 64; ++c) tma_load_2d(dst + c * 8192, tm_b, bar, n0 + 64 * c, 64 * k);
+    const int c0 = n0 + (CG == 2 ? rank * gemm_mma_cols<MODE, CG>(p, n0) / 2 : 0);
+    if constexpr (MODE == kLinear) {
+      load(dst, 64 * k, c0);
+    } else {
+      const int chunks = gemm_b_bytes(MODE, CG, p.bn) / 8192;
+      for (int c = 0; c < chunks; ++c) load(dst + c * 8192, c0 + 64 * c, 64 * k);
+    }
   }
 }
 
-// Work item i: column tile i % n_tiles, row tiles i / n_tiles + splits * j.
-// Items that run at the same time so share their x rows (one read from HBM
-// serves all column tiles), and a CTA keeps its column tile's weights.
-// grid min(items, SMs), block kGemmThreads, dynamic smem gemm_smem_bytes().
-template <int MODE, int ACT, bool RES, bool PRE>
+// Work item i: column tile i % n_tiles, row tiles (of 128 CG rows) i / n_tiles +
+// splits * j.  Items that run at the same time so share their x rows (one read
+// from HBM serves all column tiles), and a CTA keeps its column tile's weights.
+// CG = 2: the CTA pairs of clusters of two; an MMA of 256 rows reads each
+// CTA's half of B once for both, so B's shared-memory reads and its loads from
+// L2 halve (the MMA of 128 x 256 alone takes 96 of the 128 bytes per clock of
+// shared memory).
+// grid CG * min(items, SMs / CG), block kGemmThreads, dynamic smem
+// gemm_smem_bytes().
+template <int MODE, int ACT, bool RES, bool PRE, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_y,
@@ -234,15 +361,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const __grid_constant__ CUtensorMap tm_res, const GemmParams p) {
   extern __shared__ uint8_t gemm_raw[];
   uint8_t* base = gemm_raw + ((1024u - (smem_u32(gemm_raw) & 1023u)) & 1023u);
-  const uint32_t b_bytes = static_cast<uint32_t>(p.bn) * 128u;
+  const uint32_t b_bytes = gemm_b_bytes(MODE, CG, p.bn);
   const uint32_t stage_bytes = kGemmATile + (p.b_resident ? 0u : b_bytes);
   uint8_t* s_res = base + p.stages * stage_bytes;
   uint8_t* s_stage = s_res + (p.b_resident ? p.k_steps * b_bytes : 0u);
   GemmBars& bb = *reinterpret_cast<GemmBars*>(s_stage + (RES ? 2 : 1) * kGemmStaging);
   volatile int* ab = &bb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
   const int tn = gemm_tile_cols<MODE>(p);
   const int items = p.n_tiles * p.splits;
+  const int my_row = 128 * rank;   // of the tile's 128 CG rows
   const uint64_t lim = p.wait_limit_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -251,7 +381,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bb.acc_full[i], 1);
-      mbar_init(&bb.acc_free[i], kGemmEpiWarps);
+      mbar_init(&bb.acc_free[i], CG * kGemmEpiWarps);
     }
     mbar_init(&bb.b_full, 1);
     mbar_init(&bb.b_free, 1);
@@ -265,10 +395,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&tm_y);
   }
-  if (warp == kGemmMmaWarp) {
-    tmem_alloc(&bb.tmem, 512);
-    tmem_relinquish();
-  }
+  if (CG == 2) cluster_sync();   // the other CTA's barriers are ready too
+  if (warp == kGemmMmaWarp) pair_tmem_alloc<CG>(&bb.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -276,26 +404,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == kGemmTmaWarp) {
     // ---------------------------------------------------------- TMA producer
+    // In a pair both CTAs load their shares; CTA 0's barriers count all bytes.
     if (lane == 0) {
       bool ok = true;
       int q = 0, st = 0, n_item = 0;   // running load number, its stage
       uint32_t ph = 1;                 // parity of the previous use of the stage
-      for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
+      const uint32_t pair_b = CG == 2 ? cluster_addr(&bb.b_full, 0) : 0u;
+      for (int it = worker; ok && it < items; it += workers, ++n_item) {
         const int n0 = (it % p.n_tiles) * tn;
         if (p.b_resident) {
           if (n_item > 0 && !(ok = mbar_wait(&bb.b_free, (n_item - 1) & 1, ab, lim, SITE_GEMM)))
             break;
-          mbar_arrive_expect_tx(&bb.b_full, p.k_steps * b_bytes);
+          if (rank == 0) mbar_arrive_expect_tx(&bb.b_full, CG * p.k_steps * b_bytes);
           for (int k = 0; k < p.k_steps; ++k)
-            gemm_load_b<MODE>(s_res + k * b_bytes, &tm_b, &bb.b_full, p, n0, k);
+            gemm_load_b<MODE, CG>(s_res + k * b_bytes, &tm_b, &bb.b_full, pair_b, p, n0, k, rank);
         }
         for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits)
           for (int k = 0; k < p.k_steps; ++k) {
             if (q >= p.stages && !(ok = mbar_wait(&bb.empty[st], ph, ab, lim, SITE_GEMM))) break;
             uint8_t* sa = base + st * stage_bytes;
-            mbar_arrive_expect_tx(&bb.full[st], stage_bytes);
-            tma_load_2d(sa, &tm_a, &bb.full[st], 64 * k, 128 * m);
-            if (!p.b_resident) gemm_load_b<MODE>(sa + kGemmATile, &tm_b, &bb.full[st], p, n0, k);
+            if (rank == 0) mbar_arrive_expect_tx(&bb.full[st], CG * stage_bytes);
+            uint32_t pair_f = 0u;
+            if constexpr (CG == 1) {
+              tma_load_2d(sa, &tm_a, &bb.full[st], 64 * k, 128 * m);
+            } else {
+              pair_f = cluster_addr(&bb.full[st], 0);
+              tma_load_2d_pair(sa, &tm_a, pair_f, 64 * k, 256 * m + my_row);
+            }
+            if (!p.b_resident)
+              gemm_load_b<MODE, CG>(sa + kGemmATile, &tm_b, &bb.full[st], pair_f, p, n0, k, rank);
             ++q;
             if (++st == p.stages) {
               st = 0;
@@ -304,25 +441,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
       }
       if (*ab) {
-        // loads still in flight land before the CTA exits
+        // loads still in flight land before the CTA exits (in a pair, CTA 0's
+        // barriers see both CTAs' and the CTAs leave together)
         volatile int no_abort = 0;
-        if (p.b_resident && n_item > 0)
-          mbar_wait(&bb.b_full, (n_item - 1) & 1, &no_abort, 200000000ull, SITE_GEMM);
-        for (int i = max(0, q - p.stages); i < q; ++i)
-          mbar_wait(&bb.full[i % p.stages], (i / p.stages) & 1, &no_abort, 200000000ull, SITE_GEMM);
+        if (rank == 0) {
+          if (p.b_resident && n_item > 0)
+            mbar_wait(&bb.b_full, (n_item - 1) & 1, &no_abort, 200000000ull, SITE_GEMM);
+          for (int i = max(0, q - p.stages); i < q; ++i)
+            mbar_wait(&bb.full[i % p.stages], (i / p.stages) & 1, &no_abort, 200000000ull,
+                      SITE_GEMM);
+        } else {
+          // CTA 0 may have stopped counting: far longer than a load takes
+          for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
+          }
+        }
       }
     }
   } else if (warp == kGemmMmaWarp) {
     // ---------------------------------------------------------- MMA issue
+    if (rank == 0) {
     const int last_steps = (p.K - 64 * (p.k_steps - 1) + 15) / 16;
     bool ok = true;
     int st = 0, t = 0, n_item = 0;
     uint32_t ph = 0;
-    for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
+    for (int it = worker; ok && it < items; it += workers, ++n_item) {
       const int n0 = (it % p.n_tiles) * tn;
-      // a last column tile narrower than bn takes a narrower MMA
-      const int cols = MODE == kGated ? p.bn : min(p.bn, ((p.N - n0 + 15) >> 4) << 4);
-      const uint32_t idesc = make_idesc_bf16(128, cols, false, MODE == kDx);
+      const uint32_t idesc =
+          make_idesc_bf16(128 * CG, gemm_mma_cols<MODE, CG>(p, n0), false, MODE == kDx);
       if (p.b_resident && !(ok = warp_wait(&bb.b_full, n_item & 1, ab, lim, SITE_GEMM))) break;
       for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
         const int a = t & 1;
@@ -340,22 +485,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                           : make_sdesc(sb, 16, 1024, kLayoutSW128);
           const int steps = k + 1 == p.k_steps ? last_steps : 4;
           for (int s = 0; s < steps; ++s)
-            umma_ss_elect(tmem + 256 * a, ad + 2 * s, bd + (MODE == kDx ? 128 : 2) * s, idesc,
+            pair_umma<CG>(tmem + 256 * a, ad + 2 * s, bd + (MODE == kDx ? 128 : 2) * s, idesc,
                           (k > 0 || s > 0) ? 1u : 0u);
-          umma_commit_elect(&bb.empty[st]);
+          pair_commit<CG>(&bb.empty[st]);
           if (++st == p.stages) {
             st = 0;
             ph ^= 1;
           }
         }
-        if (ok) umma_commit_elect(&bb.acc_full[a]);
+        if (ok) pair_commit<CG>(&bb.acc_full[a]);
       }
-      if (ok && p.b_resident) umma_commit_elect(&bb.b_free);
+      if (ok && p.b_resident) pair_commit<CG>(&bb.b_free);
     }
     // every MMA issued above completes before the tensor memory is freed
-    umma_commit_elect(&bb.drain);
+    pair_commit<CG>(&bb.drain);
     volatile int no_abort = 0;
     mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_GEMM);
+    }
   } else {
     // ---------------------------------------------------------- epilogue
     // A tile's columns fall into units of 32; warp w takes TMEM lane quarter
@@ -374,6 +520,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     auto cell = [&](uint8_t* base, int g) {
       return reinterpret_cast<uint4*>(base + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4));
     };
+    // the accumulator's columns are read: to the CTA that issues the MMAs
+    auto free_acc = [&](int a) {
+      if constexpr (CG == 1)
+        mbar_arrive(&bb.acc_free[a]);
+      else
+        mbar_arrive_remote(cluster_addr(&bb.acc_free[a], 0));
+    };
     int t = 0;
     int turn = 0;          // group whose turn the tile's first unit is
     uint32_t res_ph = 0;   // parity of the next residual unit
@@ -381,16 +534,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     auto load_res = [&](int m, int col) {   // one unit ahead; rows and columns outside are zeros
       if (lane == 0) {
         mbar_arrive_expect_tx(&bb.res[warp], kGemmUnit);
-        tma_load_2d(sr, &tm_res, &bb.res[warp], col, 128 * m + 32 * quarter);
+        tma_load_2d(sr, &tm_res, &bb.res[warp], col, 128 * CG * m + my_row + 32 * quarter);
       }
       res_ahead = true;
     };
-    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+    for (int it = worker; ok && it < items; it += workers) {
       const int n0 = (it % p.n_tiles) * tn;
       const int units = (min(tn, p.N - n0) + 31) / 32;
       for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
         const int a = t & 1;
-        const int row0 = 128 * m + 32 * quarter;
+        const int row0 = 128 * CG * m + my_row + 32 * quarter;
         const int first = (group - turn) & 3;
         turn = (turn + units) & 3;
         // the group's first unit of the next row tile of this item
@@ -426,7 +579,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (h == 1 && u + 4 >= units) {   // this warp has read its last columns
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&bb.acc_free[a]);
+              if (lane == 0) free_acc(a);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -474,7 +627,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if constexpr (RES) {   // every lane has read its residual (put's barriers)
               if (u + 4 < units)
                 load_res(m, col + 128);
-              else if (next_m < p.m_tiles && next_first < units && 128 * next_m + 32 * quarter < p.M)
+              else if (next_m < p.m_tiles && next_first < units && row0 + 128 * CG * p.splits < p.M)
                 load_res(next_m, n0 + 32 * next_first);
             }
           }
@@ -482,7 +635,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (first >= units) {   // no unit of this tile for this warp
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bb.acc_free[a]);
+          if (lane == 0) free_acc(a);
         }
       }
     }
@@ -495,9 +648,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA of a pair leaves while the other may still read its shared
+  // memory or arrive on its barriers
+  if (CG == 2) cluster_sync();
   if (warp == kGemmMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    pair_tmem_dealloc<CG>(tmem, 512);
   }
 }
 

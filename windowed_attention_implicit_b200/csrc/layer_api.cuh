@@ -51,35 +51,45 @@ int pick_splits(int m_tiles, int n_tiles, int sms) {
 }
 
 struct GemmPlan {
-  int bn, m_tiles, n_tiles, splits, k_steps, stages, grid;
+  int cg, bn, m_tiles, n_tiles, splits, k_steps, stages, grid;
   bool resident;
   size_t smem;
 };
 
-GemmPlan plan_gemm(int M, int N, int K, bool gated, bool res, int sms) {
+GemmPlan plan_gemm(int mode, int M, int N, int K, bool res, int sms) {
   GemmPlan g{};
-  g.m_tiles = div_up(M, 128);
   g.k_steps = div_up(K, 64);
+  const bool gated = mode == kGated;
   const int unit = gated ? 128 : 64;             // bn is a multiple of this
   const int cols = gated ? 2 * N : N;
-  // The tile width with the least work on the busiest CTA: tiles per CTA times
-  // a tile's cost, its columns plus about 48 for the x rows that every
-  // column tile reads again.
+  // One CTA or a pair per tile, and the tile width: the least work on the
+  // busiest worker, tiles times a tile's cost, its columns plus a fixed part
+  // (the x rows that every column tile reads again, the pipeline's ends) worth
+  // about 48 columns.  A pair, whose MMA shares B, runs a tile better the more
+  // k-steps it has: 147456 x 384 -> 192 33 us (one CTA: 38), 8192 x 4096 -> 4096
+  // with a residual 197 us (229), 5003 x 1032 -> 2056 28.4 us (34.6); at three
+  // k-steps its longer hand-over costs more than that (147456 x 192 -> 576
+  // 46.2 us, one CTA 42.7).
   long long best = -1;
-  for (int bn = unit; bn <= 256; bn += unit) {
-    const int n_tiles = div_up(cols, bn), splits = pick_splits(g.m_tiles, n_tiles, sms);
-    const long long cost = (long long)div_up((long long)n_tiles * splits, sms) *
-                           div_up(g.m_tiles, splits) * (bn + 48);
-    if (best < 0 || cost < best) {
-      best = cost;
-      g.bn = bn;
-      g.n_tiles = n_tiles;
-      g.splits = splits;
+  for (int cg = 1; cg <= 2; ++cg) {
+    if (cg == 2 && M <= 128) break;
+    const int m_tiles = div_up(M, 128 * cg), workers = sms / cg;
+    for (int bn = unit; bn <= 256; bn += unit) {
+      const int n_tiles = div_up(cols, bn), splits = pick_splits(m_tiles, n_tiles, workers);
+      const long long cost = (long long)div_up((long long)n_tiles * splits, workers) *
+                             div_up(m_tiles, splits) * (bn + (cg == 1 ? 48 : 24 + 120 / g.k_steps));
+      if (best < 0 || cost < best) {
+        best = cost;
+        g.cg = cg;
+        g.bn = bn;
+        g.m_tiles = m_tiles;
+        g.n_tiles = n_tiles;
+        g.splits = splits;
+      }
     }
   }
-  const int items = g.n_tiles * g.splits;
-  g.grid = items < sms ? items : sms;
-  const size_t b = (size_t)g.bn * 128;
+  g.grid = std::min(g.n_tiles * g.splits, sms / g.cg) * g.cg;
+  const size_t b = gemm_b_bytes(mode, g.cg, g.bn);
   const size_t room = kSmemMax - gemm_smem_bytes(0, 0, 0, false, res);
   // weights stay in shared memory over an item's row tiles when at least
   // four stages of x still fit beside them
@@ -87,7 +97,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool gated, bool res, int sms) {
   const size_t left = room - (g.resident ? g.k_steps * b : 0);
   g.stages = static_cast<int>(left / (kGemmATile + (g.resident ? 0 : b)));
   if (g.stages > kGemmMaxStages) g.stages = kGemmMaxStages;
-  g.smem = gemm_smem_bytes(g.bn, g.stages, g.k_steps, g.resident, res);
+  g.smem = gemm_smem_bytes((uint32_t)b, g.stages, g.k_steps, g.resident, res);
   return g;
 }
 
@@ -100,13 +110,13 @@ int map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint3
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, sw);
 }
 
-template <int MODE, int ACT, bool RES, bool PRE>
+template <int MODE, int ACT, bool RES, bool PRE, int CG>
 int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
                 const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
   CUtensorMap ta, tb, ty, tp, tr;
   int rc = map_2d(&ta, a, M, K, 64, 128);
   if (!rc)
-    rc = MODE == kLinear ? map_2d(&tb, b, N, K, 64, g.bn)
+    rc = MODE == kLinear ? map_2d(&tb, b, N, K, 64, g.bn / CG)
          : MODE == kGated ? map_2d(&tb, b, 2ull * N, K, 64, g.bn / 2)
                           : map_2d(&tb, b, K, N, 64, 64);
   if (!rc) rc = map_2d(&ty, y, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -121,9 +131,28 @@ int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, con
   p.m_tiles = g.m_tiles; p.n_tiles = g.n_tiles; p.splits = g.splits;
   p.k_steps = g.k_steps; p.stages = g.stages; p.b_resident = g.resident;
   p.wait_limit_ns = g_wait_limit_ns;
-  if ((rc = set_smem(gemm_kernel<MODE, ACT, RES, PRE>, g.smem))) return rc;
+  auto kernel = gemm_kernel<MODE, ACT, RES, PRE, CG>;
+  if ((rc = set_smem(kernel, g.smem))) return rc;
   TraceScope ts(kid, st);
-  gemm_kernel<MODE, ACT, RES, PRE><<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, tr, p);
+  if constexpr (CG == 1) {
+    kernel<<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, tr, p);
+  } else {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(g.grid);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = g.smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, tp, tr, p) != cudaSuccess) {
+      cudaGetLastError();
+      return RIB_ERR_CUDA;
+    }
+  }
   return launch_status();
 }
 
@@ -132,8 +161,11 @@ int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, con
 template <int MODE, int ACT>
 int launch_gemm(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
                 const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
-#define RIB_GEMM(res, save) \
-  return launch_gemm_as<MODE, ACT, res, save>(kid, g, a, b, bias, residual, pre, y, M, N, K, st)
+#define RIB_GEMM(res, save)                                                                       \
+  return g.cg == 2 ? launch_gemm_as<MODE, ACT, res, save, 2>(kid, g, a, b, bias, residual, pre, y, \
+                                                             M, N, K, st)                         \
+                   : launch_gemm_as<MODE, ACT, res, save, 1>(kid, g, a, b, bias, residual, pre, y, \
+                                                             M, N, K, st)
   if constexpr (MODE == kLinear) {
     if (residual && pre) RIB_GEMM(true, true);
     if (pre) RIB_GEMM(false, true);
@@ -572,7 +604,7 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
-  const GemmPlan g = plan_gemm(rows, N, K, false, residual != nullptr, sms);
+  const GemmPlan g = plan_gemm(kLinear, rows, N, K, residual != nullptr, sms);
   return launch_gemm_act<kLinear>(act, K_LINEAR, g, x, w, bias, residual, pre, y, rows, N, K,
                                   static_cast<cudaStream_t>(stream));
 }
@@ -625,7 +657,7 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     }
   }
   if (dx) {
-    const GemmPlan g = plan_gemm(rows, K, N, false, dx_add != nullptr, sms);
+    const GemmPlan g = plan_gemm(kDx, rows, K, N, dx_add != nullptr, sms);
     rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, dz, w, nullptr, dx_add, nullptr, dx, rows, K,
                                     N, st);
     if (rc) return rc;
@@ -656,11 +688,11 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const GemmPlan g = plan_gemm(rows, hidden, C, true, false, sms);
+  const GemmPlan g = plan_gemm(kGated, rows, hidden, C, false, sms);
   rc = launch_gemm_act<kGated>(act, K_GATED, g, x, w_in, b_in, nullptr, nullptr, workspace, rows,
                                hidden, C, st);
   if (rc) return rc;
-  const GemmPlan o = plan_gemm(rows, C, hidden, false, residual != nullptr, sms);
+  const GemmPlan o = plan_gemm(kLinear, rows, C, hidden, residual != nullptr, sms);
   return launch_gemm<kLinear, kActNone>(K_LINEAR, o, workspace, w_out, b_out, residual, nullptr, y,
                                         rows, C, hidden, st);
 }
@@ -713,7 +745,7 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
         p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr);
     if ((rc = launch_status())) return rc;
   }
-  const GemmPlan g = plan_gemm(rows, C, 2 * hidden, false, dx_add != nullptr, sms);
+  const GemmPlan g = plan_gemm(kDx, rows, C, 2 * hidden, dx_add != nullptr, sms);
   rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, ws + L.d, w_in, nullptr, dx_add, nullptr, dx,
                                   rows, C, 2 * hidden, st);
   if (rc) return rc;
