@@ -660,35 +660,49 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ---------------------------------------------------------------- dW, db
 // dW[n][k] = sum_r dz[r][n] x[r][k] and db[n] = sum_r dz[r][n]: the rows are
 // the contraction, so both operands are MN-major (64 rows of 64 channels are
-// one canonical 8 KB atom column).  A CTA takes a tile of 256 x 192 of dW (two
-// accumulators of 128 rows) and a range of the rows; the ranges' partial
+// one canonical 8 KB atom column).  A CTA takes a tile of up to 256 x 192 of dW
+// (accumulators of 128 rows) and a range of the rows; the ranges' partial
 // sums go to the workspace and dw_reduce_kernel adds them in order.  db is
 // one more column of the product: a block of ones stands behind x's channels
-// in each stage, so the sum of the bf16 dz is exact up to fp32 accumulation
-// and costs 16 of 208 MMA columns and no pass over dz.
-constexpr int kDwThreads = 320;
-constexpr int kDwStages = 3;
+// in each stage, so the sum of the bf16 dz costs 16 of 208 MMA columns and no
+// pass over dz.
+//
+// The tensor core truncates when it adds to its accumulator, so a long chain
+// of additions drifts towards zero: 188 of them (3000 rows) left dW with a
+// relative error of 3.3e-6.  Every kDwFlush stages (32 additions) the epilogue
+// warps therefore move the accumulators into fp32 registers, added to
+// nearest, and the next chain starts from zero: 0.6e-6, as a plain fp32 sum,
+// for a stall of about a tenth of the MMAs' time, which the loads hide.
+constexpr int kDwThreads = 384;   // warps 0-7 epilogue, 8 TMA, 9 MMA, two idle
 constexpr int kDwBn = 192;
+constexpr int kDwFlush = 8;
 constexpr uint32_t kDwAtom = 8192;                       // 64 rows x 64 channels
-constexpr uint32_t kDwStageBytes = (4 + 4) * kDwAtom;    // dz: 4 atoms; x: 3, ones: 1
+constexpr int kDwMaxStages = 8;
+// Registers (setmaxnreg): 256 x 224 + 128 x 56 = 64512 = 384 x 168 at launch.
+constexpr int kDwEpiRegs = 224, kDwOtherRegs = 56;
 
 struct DwParams {
   int rows, N, K;
-  int m_tiles, n_tiles, splits;
+  int a_chunks, b_chunks;          // 64-channel chunks of a tile: dz (2 .. 4), x (1 .. 3)
+  int m_tiles, n_tiles, splits, stages;
   int steps, steps_per_split;      // 64-row steps, in all and per split
-  float* part;                     // [splits][N][K]
+  float* part;                     // [splits][N][K]; with one split dW itself, if fp32
+  __nv_bfloat16* out16;            // one split and a bf16 dW
   float* part_db;                  // [splits][N]; null: no db
   uint64_t wait_limit_ns;
 };
 
 struct DwBars {
-  uint64_t full[kDwStages], empty[kDwStages], acc_full, drain;
+  uint64_t full[kDwMaxStages], empty[kDwMaxStages], acc_full, acc_free, drain;
   uint32_t tmem;
   int abort_flag;
 };
 
-__host__ __device__ __forceinline__ size_t dw_smem_bytes() {
-  return 1024 + kDwStages * kDwStageBytes + sizeof(DwBars);
+__host__ __device__ __forceinline__ uint32_t dw_stage_bytes(int a_chunks, int b_chunks) {
+  return static_cast<uint32_t>(a_chunks + b_chunks + 1) * kDwAtom;   // dz, x, ones
+}
+__host__ __device__ __forceinline__ size_t dw_smem_bytes(int a_chunks, int b_chunks, int stages) {
+  return 1024 + static_cast<size_t>(stages) * dw_stage_bytes(a_chunks, b_chunks) + sizeof(DwBars);
 }
 
 // grid m_tiles * n_tiles * splits, block kDwThreads, dynamic smem dw_smem_bytes().
@@ -699,31 +713,35 @@ __global__ void __launch_bounds__(kDwThreads, 1)
               const DwParams p) {
   extern __shared__ uint8_t dwg_raw[];
   uint8_t* base = dwg_raw + ((1024u - (smem_u32(dwg_raw) & 1023u)) & 1023u);
-  DwBars& bb = *reinterpret_cast<DwBars*>(base + kDwStages * kDwStageBytes);
+  const uint32_t stage_bytes = dw_stage_bytes(p.a_chunks, p.b_chunks);
+  const uint32_t b_off = p.a_chunks * kDwAtom;
+  DwBars& bb = *reinterpret_cast<DwBars*>(base + p.stages * stage_bytes);
   volatile int* ab = &bb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = p.m_tiles * p.n_tiles;
   const int tile = blockIdx.x % tiles, split = blockIdx.x / tiles;
-  const int m0 = (tile / p.n_tiles) * 256, k0 = (tile % p.n_tiles) * kDwBn;
-  const int a_chunks = min(4, (p.N - m0 + 63) / 64), b_chunks = min(3, (p.K - k0 + 63) / 64);
-  const int blocks = p.N - m0 > 128 ? 2 : 1;
+  const int m0 = (tile / p.n_tiles) * 64 * p.a_chunks, k0 = (tile % p.n_tiles) * 64 * p.b_chunks;
+  const int a_chunks = min(p.a_chunks, (p.N - m0 + 63) / 64);
+  const int b_chunks = min(p.b_chunks, (p.K - k0 + 63) / 64);
+  const int blocks = p.a_chunks > 2 && p.N - m0 > 128 ? 2 : 1;
   const bool with_db = p.part_db != nullptr && k0 == 0;
   const int s0 = split * p.steps_per_split, s1 = min(p.steps, s0 + p.steps_per_split);
   const uint64_t lim = p.wait_limit_ns;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDwStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(&bb.full[i], 1);
       mbar_init(&bb.empty[i], 1);
     }
     mbar_init(&bb.acc_full, 1);
+    mbar_init(&bb.acc_free, 4 * blocks);
     mbar_init(&bb.drain, 1);
     bb.abort_flag = 0;
     fence_mbarrier_init();
   }
   if (with_db) {
     // ones behind x's atoms (every element: the swizzle does not matter)
-    for (int i = threadIdx.x; i < kDwStages * 512; i += kDwThreads)
-      *reinterpret_cast<uint4*>(base + (i / 512) * kDwStageBytes + (4 + b_chunks) * kDwAtom +
+    for (int i = threadIdx.x; i < p.stages * 512; i += kDwThreads)
+      *reinterpret_cast<uint4*>(base + (i / 512) * stage_bytes + b_off + b_chunks * kDwAtom +
                                 (i % 512) * 16) =
           make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     fence_proxy_async_smem();
@@ -736,84 +754,125 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bb.tmem;
-  bool ok = true;
-  if (warp == 8) {
-    if (lane == 0) {
-      int q = 0;
-      for (int s = s0; ok && s < s1; ++s, ++q) {
-        const int st = q % kDwStages;
-        if (q >= kDwStages &&
-            !(ok = mbar_wait(&bb.empty[st], (q / kDwStages - 1) & 1, ab, lim, SITE_DW)))
-          break;
-        uint8_t* sa = base + st * kDwStageBytes;
-        mbar_arrive_expect_tx(&bb.full[st], (a_chunks + b_chunks) * kDwAtom);
-        for (int c = 0; c < a_chunks; ++c)
-          tma_load_2d(sa + c * kDwAtom, &tm_z, &bb.full[st], m0 + 64 * c, 64 * s);
-        for (int c = 0; c < b_chunks; ++c)
-          tma_load_2d(sa + (4 + c) * kDwAtom, &tm_x, &bb.full[st], k0 + 64 * c, 64 * s);
-      }
-      if (*ab) {
-        volatile int no_abort = 0;
-        for (int i = max(0, q - kDwStages); i < q; ++i)
-          mbar_wait(&bb.full[i % kDwStages], (i / kDwStages) & 1, &no_abort, 200000000ull, SITE_DW);
-      }
-    }
-  } else if (warp == 9) {
-    const uint32_t idesc = make_idesc_bf16(128, 64 * b_chunks + (with_db ? 16 : 0), true, true);
-    int q = 0;
-    for (int s = s0; ok && s < s1; ++s, ++q) {
-      const int st = q % kDwStages;
-      if (!(ok = warp_wait(&bb.full[st], (q / kDwStages) & 1, ab, lim, SITE_DW))) break;
-      tc_fence_after();
-      const uint32_t sa = smem_u32(base + st * kDwStageBytes);
-      const uint64_t bd = make_sdesc(sa + 4 * kDwAtom, kDwAtom, 1024, kLayoutSW128);
-      for (int b = 0; b < blocks; ++b) {
-        const uint64_t ad = make_sdesc(sa + 2 * b * kDwAtom, kDwAtom, 1024, kLayoutSW128);
-        for (int k = 0; k < 4; ++k)
-          umma_ss_elect(tmem + 256 * b, ad + 128 * k, bd + 128 * k, idesc,
-                        (q > 0 || k > 0) ? 1u : 0u);
-      }
-      umma_commit_elect(&bb.empty[st]);
-    }
-    if (ok) umma_commit_elect(&bb.acc_full);
-    umma_commit_elect(&bb.drain);
-    volatile int no_abort = 0;
-    mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_DW);
-  } else if ((warp >> 2) < blocks) {
+  if (warp < 8) {
+    // ---------------------------------------------------------- epilogue
     // warp w: rows 32 (w % 4) .. of block w / 4, every column
-    ok = warp_wait(&bb.acc_full, 0, ab, lim, SITE_DW);
-    tc_fence_after();
-    const int blk = warp >> 2;
-    const int n = m0 + 128 * blk + 32 * (warp & 3) + lane;
-    const uint32_t acc = tmem + 256 * blk + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const size_t row = static_cast<size_t>(split) * p.N + n;
-    const size_t part_n = static_cast<size_t>(p.splits) * p.N * p.K;
-    if (ok) {
-      for (int c = 0; c < 2 * b_chunks; ++c) {
-        uint32_t v[32];
-        tmem_ld_x32(acc + 32 * c, v);
-        tmem_wait_ld();
-        reg_fence_x32(v);
-        const int k = k0 + 32 * c;
-        if (n < p.N) {
+    regs_inc<kDwEpiRegs>();
+    if ((warp >> 2) < blocks) {
+      const int blk = warp >> 2;
+      const int n = m0 + 128 * blk + 32 * (warp & 3) + lane;
+      const uint32_t acc = tmem + 256 * blk + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      float sum[kDwBn], sum_db = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const size_t at = row * p.K + k + 4 * e;
-            if (k + 4 * e < p.K && rib_guard(at + 3, part_n, G_DW_PART))
-              *reinterpret_cast<float4*>(p.part + at) =
-                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                              __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+      for (int c = 0; c < kDwBn; ++c) sum[c] = 0.f;
+      bool ok = true;
+      int f = 0;
+      for (int s = s0; s < s1; s += kDwFlush, ++f) {
+        if (!(ok = warp_wait(&bb.acc_full, f & 1, ab, lim, SITE_DW))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kDwBn / 16; ++c) {
+          if (c >= 4 * b_chunks) continue;
+          uint32_t v[16];
+          tmem_ld_x16(acc + 16 * c, v);
+          tmem_wait_ld();
+          reg_fence_x16(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[16 * c + e] += __uint_as_float(v[e]);
+        }
+        if (with_db) {
+          uint32_t v[16];
+          tmem_ld_x16(acc + 64 * b_chunks, v);
+          tmem_wait_ld();
+          reg_fence_x16(v);
+          sum_db += __uint_as_float(v[0]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bb.acc_free);
+      }
+      // this thread's row of the tile (a tile of three chunks ends inside its
+      // second block, whose other rows are the next tile's)
+      const int n_end = min(p.N, m0 + 64 * p.a_chunks);
+      const size_t row = static_cast<size_t>(split) * p.N + n;
+      const size_t part_n = static_cast<size_t>(p.splits) * p.N * p.K;
+      if (ok && n < n_end) {
+#pragma unroll
+        for (int c = 0; c < kDwBn / 4; ++c) {
+          const int k = k0 + 4 * c;
+          const size_t at = row * p.K + k;
+          if (c >= 16 * b_chunks || k >= p.K || !rib_guard(at + 3, part_n, G_DW_PART)) continue;
+          if (p.out16)
+            *reinterpret_cast<uint2*>(p.out16 + at) =
+                make_uint2(pack_bf16x2(sum[4 * c], sum[4 * c + 1]),
+                           pack_bf16x2(sum[4 * c + 2], sum[4 * c + 3]));
+          else
+            *reinterpret_cast<float4*>(p.part + at) =
+                make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]);
+        }
+        if (with_db && rib_guard(row, static_cast<size_t>(p.splits) * p.N, G_DW_PART))
+          p.part_db[row] = sum_db;
+      }
+    }
+  } else {
+    regs_dec<kDwOtherRegs>();
+    bool ok = true;
+    if (warp == 8) {
+      // -------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        int q = 0, st = 0;
+        uint32_t ph = 1;
+        for (int s = s0; s < s1; ++s, ++q) {
+          if (q >= p.stages && !(ok = mbar_wait(&bb.empty[st], ph, ab, lim, SITE_DW))) break;
+          uint8_t* sa = base + st * stage_bytes;
+          mbar_arrive_expect_tx(&bb.full[st], (a_chunks + b_chunks) * kDwAtom);
+          for (int c = 0; c < a_chunks; ++c)
+            tma_load_2d(sa + c * kDwAtom, &tm_z, &bb.full[st], m0 + 64 * c, 64 * s);
+          for (int c = 0; c < b_chunks; ++c)
+            tma_load_2d(sa + b_off + c * kDwAtom, &tm_x, &bb.full[st], k0 + 64 * c, 64 * s);
+          if (++st == p.stages) {
+            st = 0;
+            ph ^= 1;
           }
         }
+        if (*ab) {
+          volatile int no_abort = 0;
+          for (int i = max(0, q - p.stages); i < q; ++i)
+            mbar_wait(&bb.full[i % p.stages], (i / p.stages) & 1, &no_abort, 200000000ull, SITE_DW);
+        }
       }
-      if (with_db) {
-        uint32_t v[16];
-        tmem_ld_x16(acc + 64 * b_chunks, v);
-        tmem_wait_ld();
-        reg_fence_x16(v);
-        if (n < p.N && rib_guard(row, static_cast<size_t>(p.splits) * p.N, G_DW_PART))
-          p.part_db[row] = __uint_as_float(v[0]);
+    } else if (warp == 9) {
+      // -------------------------------------------------------- MMA issue
+      const uint32_t idesc = make_idesc_bf16(128, 64 * b_chunks + (with_db ? 16 : 0), true, true);
+      int q = 0, st = 0, f = 0;
+      uint32_t ph = 0;
+      for (int s = s0; ok && s < s1; ++s, ++q) {
+        const bool fresh = q % kDwFlush == 0;
+        if (fresh && q > 0) {   // the last chain's sums leave tensor memory
+          umma_commit_elect(&bb.acc_full);
+          if (!(ok = warp_wait(&bb.acc_free, f & 1, ab, lim, SITE_DW))) break;
+          ++f;
+        }
+        if (!(ok = warp_wait(&bb.full[st], ph, ab, lim, SITE_DW))) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(base + st * stage_bytes);
+        const uint64_t bd = make_sdesc(sa + b_off, kDwAtom, 1024, kLayoutSW128);
+        for (int b = 0; b < blocks; ++b) {
+          const uint64_t ad = make_sdesc(sa + 2 * b * kDwAtom, kDwAtom, 1024, kLayoutSW128);
+          for (int k = 0; k < 4; ++k)
+            umma_ss_elect(tmem + 256 * b, ad + 128 * k, bd + 128 * k, idesc,
+                          (!fresh || k > 0) ? 1u : 0u);
+        }
+        umma_commit_elect(&bb.empty[st]);
+        if (++st == p.stages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
+      if (ok) umma_commit_elect(&bb.acc_full);
+      umma_commit_elect(&bb.drain);
+      volatile int no_abort = 0;
+      mbar_wait(&bb.drain, 0, &no_abort, 200000000ull, SITE_DW);
     }
   }
   tc_fence_before();
@@ -824,25 +883,45 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
 }
 
-// dW = sum of the splits' partials, in order; fp32 or rounded to bf16 once.
-// n = N * K (a multiple of 4); grid ceil(n / 4 / 256), block 256.
+// dW and db = the sums of the splits' partials: four groups of threads take a
+// quarter of the splits each, in order, and their sums are added in order.
+// n4 = N K / 4 float4 of dW (none when there is one split), then N / 4 of db;
+// dW fp32 or rounded to bf16 once.  grid ceil((n4 + nb4) / 64), block 256.
 __global__ void __launch_bounds__(256)
-    dw_reduce_kernel(const float* part, int splits, size_t n, float* out32, __nv_bfloat16* out16) {
-  const size_t i = 4 * (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x);
-  if (i >= n) return;
+    dw_reduce_kernel(const float* part, const float* part_db, int splits, size_t n4, size_t nb4,
+                     float* out32, __nv_bfloat16* out16, float* db) {
+  __shared__ float4 sums[4][64];
+  const int col = threadIdx.x & 63, group = threadIdx.x >> 6;
+  const size_t i = static_cast<size_t>(blockIdx.x) * 64 + col;
+  const bool is_db = i >= n4;
+  const float* src = is_db ? part_db : part;
+  const size_t n = 4 * (is_db ? nb4 : n4), at0 = 4 * (is_db ? i - n4 : i);
+  const bool in = i < n4 + nb4;
+  const int per = (splits + 3) / 4, k1 = min(splits, (group + 1) * per);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = 0; k < splits; ++k) {
-    const size_t at = static_cast<size_t>(k) * n + i;
-    if (!rib_guard(at + 3, static_cast<size_t>(splits) * n, G_DW_RED)) continue;
-    const float4 v = __ldg(reinterpret_cast<const float4*>(part + at));
+  if (in) {
+#pragma unroll 4
+    for (int k = group * per; k < k1; ++k) {
+      const size_t at = static_cast<size_t>(k) * n + at0;
+      if (!rib_guard(at + 3, static_cast<size_t>(splits) * n, G_DW_RED)) continue;
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + at));
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  }
+  sums[group][col] = s;
+  __syncthreads();
+  if (group != 0 || !in) return;
+#pragma unroll
+  for (int g = 1; g < 4; ++g) {
+    const float4 v = sums[g][col];
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
-  if (out32) {
-    *reinterpret_cast<float4*>(out32 + i) = s;
-  } else {
-    *reinterpret_cast<uint2*>(out16 + i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-  }
+  if (is_db)
+    *reinterpret_cast<float4*>(db + at0) = s;
+  else if (out32)
+    *reinterpret_cast<float4*>(out32 + at0) = s;
+  else
+    *reinterpret_cast<uint2*>(out16 + at0) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
 // ---------------------------------------------------------------- dz

@@ -192,32 +192,41 @@ int launch_gemm_act(int act, int kid, const GemmPlan& g, const void* a, const vo
 }
 
 struct DwPlan {
-  int m_tiles, n_tiles, splits, steps, per_split;
+  int a_chunks, b_chunks, stages, m_tiles, n_tiles, splits, steps, per_split;
   size_t part, part_db;   // bytes
 };
 
-// dW [N][K] over `rows` rows.  More splits shorten the rows' loop and
-// lengthen the sum of the partials: the count with the smallest estimate of
-// both (about 0.6 us per 64-row step of a full tile, 4 TB/s for the partials
-// written and read).
+// dW [N][K] over `rows` rows: the tile's height (the one that divides N best)
+// and the number of row ranges.  More ranges shorten the rows' loop and
+// lengthen the sum of the partials; the estimate of both that is minimised
+// takes 0.15 us per 8 KB atom loaded (or the MMAs' 0.32 us per 64 rows and
+// accumulator, if longer) and 4 TB/s for partials written and read.
 DwPlan plan_dw(int rows, int N, int K, int sms) {
   DwPlan d{};
-  d.m_tiles = div_up(N, 256);
-  d.n_tiles = div_up(K, kDwBn);
   d.steps = div_up(rows, 64);
-  const long long tiles = (long long)d.m_tiles * d.n_tiles;
+  d.b_chunks = std::min(kDwBn / 64, div_up(K, 64));
+  d.n_tiles = div_up(K, 64 * d.b_chunks);
   double best = -1.0;
-  for (int s = 1; s <= d.steps && (s == 1 || tiles * s <= 2ll * sms); ++s) {
-    const int per = div_up(d.steps, s);
-    const double cost = div_up(tiles * s, sms) * (per + 4) * 0.6 +
-                        (double)s * N * K * 8.0 / 4.0e6;
-    if (best < 0 || cost < best) {
-      best = cost;
-      d.per_split = per;
-      d.splits = div_up(d.steps, per);   // no empty range
+  for (int ac = 2; ac <= 4; ++ac) {
+    const int m_tiles = div_up(N, 64 * ac);
+    const long long tiles = (long long)m_tiles * d.n_tiles;
+    const double step = std::max(0.15 * (ac + d.b_chunks), 0.32 * (ac > 2 ? 2 : 1));
+    for (int s = 1; s <= d.steps && (s == 1 || tiles * s <= 2ll * sms); ++s) {
+      const int per = div_up(d.steps, s);
+      const double cost = div_up(tiles * s, sms) * (per + 4) * step +
+                          (s > 1 ? 2.0 + (double)s * N * K * 8.0 / 4.0e6 : 0.0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        d.a_chunks = ac;
+        d.m_tiles = m_tiles;
+        d.per_split = per;
+        d.splits = div_up(d.steps, per);   // no empty range
+      }
     }
   }
-  d.part = align256((size_t)d.splits * N * K * 4);
+  d.stages = std::min<int>(kDwMaxStages, (kSmemMax - dw_smem_bytes(0, 0, 0)) /
+                                             dw_stage_bytes(d.a_chunks, d.b_chunks));
+  d.part = d.splits > 1 ? align256((size_t)d.splits * N * K * 4) : 0;
   d.part_db = align256((size_t)d.splits * N * 4);
   return d;
 }
@@ -229,36 +238,30 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   int rc = map_2d(&tz, dz, rows, N, 64, 64);
   if (!rc) rc = map_2d(&tx, x, rows, K, 64, 64);
   if (rc) return rc;
+  const bool f32 = dw_dtype == RIB_DTYPE_F32, direct = d.splits == 1;
   DwParams p{};
   p.rows = rows; p.N = N; p.K = K;
-  p.m_tiles = d.m_tiles; p.n_tiles = d.n_tiles; p.splits = d.splits;
+  p.a_chunks = d.a_chunks; p.b_chunks = d.b_chunks;
+  p.m_tiles = d.m_tiles; p.n_tiles = d.n_tiles; p.splits = d.splits; p.stages = d.stages;
   p.steps = d.steps; p.steps_per_split = d.per_split;
-  p.part = static_cast<float*>(part);
-  p.part_db = db ? static_cast<float*>(part_db) : nullptr;
+  p.part = static_cast<float*>(direct ? (f32 ? dw : nullptr) : part);
+  p.out16 = direct && !f32 ? static_cast<__nv_bfloat16*>(dw) : nullptr;
+  p.part_db = !db ? nullptr : direct ? db : static_cast<float*>(part_db);
   p.wait_limit_ns = g_wait_limit_ns;
-  const size_t smem = dw_smem_bytes();
+  const size_t smem = dw_smem_bytes(d.a_chunks, d.b_chunks, d.stages);
   if ((rc = set_smem(dw_kernel, smem))) return rc;
   {
     TraceScope ts(K_DW, st);
     dw_kernel<<<d.m_tiles * d.n_tiles * d.splits, kDwThreads, smem, st>>>(tz, tx, p);
     if ((rc = launch_status())) return rc;
   }
-  {
-    TraceScope ts(K_DW_RED, st);
-    const size_t n = (size_t)N * K;
-    const bool f32 = dw_dtype == RIB_DTYPE_F32;
-    dw_reduce_kernel<<<div_up((long long)n / 4, 256), 256, 0, st>>>(
-        p.part, d.splits, n, f32 ? static_cast<float*>(dw) : nullptr,
-        f32 ? nullptr : static_cast<__nv_bfloat16*>(dw));
-    if ((rc = launch_status())) return rc;
-  }
-  if (db) {
-    TraceScope ts(K_ROWS_RED, st);
-    reduce_rows_kernel<<<div_up(N, 32), kLnThreads, 0, st>>>(p.part_db, d.splits, N, db, 0,
-                                                             nullptr);
-    rc = launch_status();
-  }
-  return rc;
+  if (direct) return rc;
+  TraceScope ts(K_DW_RED, st);
+  const size_t n4 = (size_t)N * K / 4, nb4 = db ? N / 4 : 0;
+  dw_reduce_kernel<<<div_up((long long)(n4 + nb4), 64), 256, 0, st>>>(
+      p.part, p.part_db, d.splits, n4, nb4, f32 ? static_cast<float*>(dw) : nullptr,
+      f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db);
+  return launch_status();
 }
 
 bool aligned16_all(std::initializer_list<const void*> ptrs) {
