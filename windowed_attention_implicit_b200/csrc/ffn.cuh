@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     bool ok = true;
     int st = 0, t = 0, n_item = 0;
     uint32_t ph = 0;
+    RingWait ring;
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
       if (p.b_resident && !(ok = warp_wait(&bb.b_full, n_item & 1, ab, lim, SITE_FFN))) break;
       for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         if (t >= 2 && !(ok = warp_wait(&bb.acc_free[a], ((t >> 1) - 1) & 1, ab, lim, SITE_FFN)))
           break;
         for (int k = 0; k < p.k_steps; ++k) {
-          if (!(ok = warp_wait(&bb.full[st], ph, ab, lim, SITE_FFN))) break;
+          if (!(ok = ring.wait(&bb.full[st], ph, ab, lim, SITE_FFN))) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(base + st * stage_bytes);
           const uint32_t sb = p.b_resident ? smem_u32(s_res + k * kFfnB) : sa + kFfnA;
@@ -182,16 +183,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           const uint64_t wd = make_sdesc(sb, 16, 1024, kLayoutSW128);
           const uint64_t od = make_sdesc(sb + 16384, 8192, 1024, kLayoutSW128);
           const int steps = k + 1 == p.k_steps ? last_steps : 4;
-          for (int s = 0; s < steps; ++s) {
-            const uint32_t acc = (k > 0 || s > 0) ? 1u : 0u;
-            umma_ss_elect(tmem + 256 * a, xd + 2 * s, wd + 2 * s, id_gu, acc);
-            umma_ss_elect(tmem + 256 * a + 128, yd + 2 * s, od + 128 * s, id_dh, acc);
-          }
-          umma_commit_elect(&bb.empty[st]);
+          uint64_t* done = &bb.empty[st];
           if (++st == p.stages) {
             st = 0;
             ph ^= 1;
           }
+          ring.peek(&bb.full[st], ph);
+          const uint32_t acc = k > 0 ? 1u : 0u;
+          pair_umma_steps<1>(steps, tmem + 256 * a, xd, 2, wd, 2, id_gu, acc);
+          pair_umma_steps<1>(steps, tmem + 256 * a + 128, yd, 2, od, 128, id_dh, acc);
+          umma_commit_elect(done);
         }
         if (ok) umma_commit_elect(&bb.acc_full[a]);
       }

@@ -123,6 +123,76 @@ __device__ __forceinline__ void pair_umma(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Four MMAs D (+)= A_k B_k, the descriptors advanced by a_step and b_step (units
+// of 16 bytes), from one election: `first_acc` = 0 makes the first overwrite D.
+// The issuing warp is a serial resource of these kernels: with an election and
+// a wait per MMA and k-step it took about 580 cycles for the 4 x 96 of a
+// k-step of 192 columns.
+#define RIB_CHAIN4(cg)                                                        \
+  asm volatile(                                                               \
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b, sa, sb;\n\t"             \
+      "setp.ne.b32 p, %6, 0;\n\t"                                            \
+      "setp.eq.b32 t, %5, %5;\n\t"                                           \
+      "cvt.u64.u32 sa, %2;\n\t cvt.u64.u32 sb, %4;\n\t"                     \
+      "elect.sync _|e, 0xffffffff;\n\t"                                      \
+      "@e tcgen05.mma.cta_group::" cg ".kind::f16 [%0], %1, %3, %5, p;\n\t"  \
+      "add.s64 a, %1, sa;\n\t add.s64 b, %3, sb;\n\t"                       \
+      "@e tcgen05.mma.cta_group::" cg ".kind::f16 [%0], a, b, %5, t;\n\t"    \
+      "add.s64 a, a, sa;\n\t add.s64 b, b, sb;\n\t"                         \
+      "@e tcgen05.mma.cta_group::" cg ".kind::f16 [%0], a, b, %5, t;\n\t"    \
+      "add.s64 a, a, sa;\n\t add.s64 b, b, sb;\n\t"                         \
+      "@e tcgen05.mma.cta_group::" cg ".kind::f16 [%0], a, b, %5, t;\n\t}" ::"r"(d), \
+      "l"(a), "r"(a_step), "l"(b), "r"(b_step), "r"(idesc), "r"(first_acc)    \
+      : "memory")
+template <int CG>
+__device__ __forceinline__ void pair_umma4(uint32_t d, uint64_t a, uint32_t a_step, uint64_t b,
+                                           uint32_t b_step, uint32_t idesc, uint32_t first_acc) {
+  if constexpr (CG == 1)
+    RIB_CHAIN4("1");
+  else
+    RIB_CHAIN4("2");
+}
+#undef RIB_CHAIN4
+// `steps` (1 .. 4) of them
+template <int CG>
+__device__ __forceinline__ void pair_umma_steps(int steps, uint32_t d, uint64_t a, uint32_t a_step,
+                                                uint64_t b, uint32_t b_step, uint32_t idesc,
+                                                uint32_t first_acc) {
+  if (steps == 4) {
+    pair_umma4<CG>(d, a, a_step, b, b_step, idesc, first_acc);
+  } else {
+    for (int s = 0; s < steps; ++s)
+      pair_umma<CG>(d, a + static_cast<uint64_t>(a_step) * s, b + static_cast<uint64_t>(b_step) * s,
+                    idesc, s > 0 ? 1u : first_acc);
+  }
+}
+
+// Waits of the issuing warp on a ring of barriers.  The next barrier is tested
+// before the MMAs of the present one are issued, so its answer is there when
+// it is asked for (test_wait: try_wait may sleep until the phase completes,
+// with the MMAs not yet issued behind it).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+struct RingWait {
+  bool ready = false;
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* ab,
+                                       uint64_t lim, int site) {
+    return __all_sync(0xffffffffu, ready) || warp_wait(bar, parity, ab, lim, site);
+  }
+  __device__ __forceinline__ void peek(uint64_t* bar, uint32_t parity) {
+    ready = mbar_test(bar, parity);
+  }
+};
+
 // Arrives on `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
 template <int CG>
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
@@ -274,6 +344,7 @@ struct GemmParams {
   int m_tiles, n_tiles;
   int splits;                      // the row tiles of one column tile go to `splits` items
   int k_steps, stages;
+  uint32_t a_bytes;                // of a k-step's x tile (rows that are not loaded are not stored)
   int b_resident;                  // the column tile's weights stay in shared memory
   uint64_t wait_limit_ns;
 };
@@ -423,7 +494,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int k = 0; k < p.k_steps; ++k) {
             if (q >= p.stages && !(ok = mbar_wait(&bb.empty[st], ph, ab, lim, SITE_GEMM))) break;
             uint8_t* sa = base + st * stage_bytes;
-            if (rank == 0) mbar_arrive_expect_tx(&bb.full[st], CG * stage_bytes);
+            if (rank == 0)
+              mbar_arrive_expect_tx(&bb.full[st], CG * (p.a_bytes + stage_bytes - kGemmATile));
             uint32_t pair_f = 0u;
             if constexpr (CG == 1) {
               tma_load_2d(sa, &tm_a, &bb.full[st], 64 * k, 128 * m);
@@ -464,6 +536,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
     int st = 0, t = 0, n_item = 0;
     uint32_t ph = 0;
+    RingWait ring;
     for (int it = worker; ok && it < items; it += workers, ++n_item) {
       const int n0 = (it % p.n_tiles) * tn;
       const uint32_t idesc =
@@ -474,7 +547,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (t >= 2 && !(ok = warp_wait(&bb.acc_free[a], ((t >> 1) - 1) & 1, ab, lim, SITE_GEMM)))
           break;
         for (int k = 0; k < p.k_steps; ++k) {
-          if (!(ok = warp_wait(&bb.full[st], ph, ab, lim, SITE_GEMM))) break;
+          if (!(ok = ring.wait(&bb.full[st], ph, ab, lim, SITE_GEMM))) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(base + st * stage_bytes);
           const uint32_t sb = p.b_resident ? smem_u32(s_res + k * b_bytes) : sa + kGemmATile;
@@ -483,15 +556,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t ad = make_sdesc(sa, 16, 1024, kLayoutSW128);
           const uint64_t bd = MODE == kDx ? make_sdesc(sb, 8192, 1024, kLayoutSW128)
                                           : make_sdesc(sb, 16, 1024, kLayoutSW128);
-          const int steps = k + 1 == p.k_steps ? last_steps : 4;
-          for (int s = 0; s < steps; ++s)
-            pair_umma<CG>(tmem + 256 * a, ad + 2 * s, bd + (MODE == kDx ? 128 : 2) * s, idesc,
-                          (k > 0 || s > 0) ? 1u : 0u);
-          pair_commit<CG>(&bb.empty[st]);
+          uint64_t* done = &bb.empty[st];
           if (++st == p.stages) {
             st = 0;
             ph ^= 1;
           }
+          ring.peek(&bb.full[st], ph);
+          pair_umma_steps<CG>(k + 1 == p.k_steps ? last_steps : 4, tmem + 256 * a, ad, 2, bd,
+                              MODE == kDx ? 128 : 2, idesc, k > 0 ? 1u : 0u);
+          pair_commit<CG>(done);
         }
         if (ok) pair_commit<CG>(&bb.acc_full[a]);
       }
@@ -846,6 +919,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       const uint32_t idesc = make_idesc_bf16(128, 64 * b_chunks + (with_db ? 16 : 0), true, true);
       int q = 0, st = 0, f = 0;
       uint32_t ph = 0;
+      RingWait ring;
       for (int s = s0; ok && s < s1; ++s, ++q) {
         const bool fresh = q % kDwFlush == 0;
         if (fresh && q > 0) {   // the last chain's sums leave tensor memory
@@ -853,21 +927,20 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           if (!(ok = warp_wait(&bb.acc_free, f & 1, ab, lim, SITE_DW))) break;
           ++f;
         }
-        if (!(ok = warp_wait(&bb.full[st], ph, ab, lim, SITE_DW))) break;
+        if (!(ok = ring.wait(&bb.full[st], ph, ab, lim, SITE_DW))) break;
         tc_fence_after();
         const uint32_t sa = smem_u32(base + st * stage_bytes);
         const uint64_t bd = make_sdesc(sa + b_off, kDwAtom, 1024, kLayoutSW128);
-        for (int b = 0; b < blocks; ++b) {
-          const uint64_t ad = make_sdesc(sa + 2 * b * kDwAtom, kDwAtom, 1024, kLayoutSW128);
-          for (int k = 0; k < 4; ++k)
-            umma_ss_elect(tmem + 256 * b, ad + 128 * k, bd + 128 * k, idesc,
-                          (!fresh || k > 0) ? 1u : 0u);
-        }
-        umma_commit_elect(&bb.empty[st]);
+        uint64_t* done = &bb.empty[st];
         if (++st == p.stages) {
           st = 0;
           ph ^= 1;
         }
+        ring.peek(&bb.full[st], ph);
+        for (int b = 0; b < blocks; ++b)
+          pair_umma4<1>(tmem + 256 * b, make_sdesc(sa + 2 * b * kDwAtom, kDwAtom, 1024, kLayoutSW128),
+                        128, bd, 128, idesc, fresh ? 0u : 1u);
+        umma_commit_elect(done);
       }
       if (ok) umma_commit_elect(&bb.acc_full);
       umma_commit_elect(&bb.drain);

@@ -10,6 +10,7 @@
 #include "layer_norm.cuh"
 #include "gemm.cuh"
 #include "ffn.cuh"
+#include "few_rows.cuh"
 
 namespace rib {
 namespace {
@@ -51,7 +52,7 @@ int pick_splits(int m_tiles, int n_tiles, int sms) {
 }
 
 struct GemmPlan {
-  int cg, bn, m_tiles, n_tiles, splits, k_steps, stages, grid;
+  int cg, bn, a_rows, m_tiles, n_tiles, splits, k_steps, stages, grid;
   bool resident;
   size_t smem;
 };
@@ -89,6 +90,8 @@ GemmPlan plan_gemm(int mode, int M, int N, int K, bool res, int sms) {
     }
   }
   g.grid = std::min(g.n_tiles * g.splits, sms / g.cg) * g.cg;
+  // a lone row tile of few rows is loaded as such
+  g.a_rows = g.cg == 1 && M < 128 ? div_up(M, 8) * 8 : 128;
   const size_t b = gemm_b_bytes(mode, g.cg, g.bn);
   const size_t room = kSmemMax - gemm_smem_bytes(0, 0, 0, false, res);
   // weights stay in shared memory over an item's row tiles when at least
@@ -114,7 +117,7 @@ template <int MODE, int ACT, bool RES, bool PRE, int CG>
 int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, const float* bias,
                 const void* residual, void* pre, void* y, int M, int N, int K, cudaStream_t st) {
   CUtensorMap ta, tb, ty, tp, tr;
-  int rc = map_2d(&ta, a, M, K, 64, 128);
+  int rc = map_2d(&ta, a, M, K, 64, g.a_rows);
   if (!rc)
     rc = MODE == kLinear ? map_2d(&tb, b, N, K, 64, g.bn / CG)
          : MODE == kGated ? map_2d(&tb, b, 2ull * N, K, 64, g.bn / 2)
@@ -129,6 +132,7 @@ int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, con
   p.M = M; p.N = N; p.K = K;
   p.bn = g.bn;
   p.m_tiles = g.m_tiles; p.n_tiles = g.n_tiles; p.splits = g.splits;
+  p.a_bytes = 128u * g.a_rows;
   p.k_steps = g.k_steps; p.stages = g.stages; p.b_resident = g.resident;
   p.wait_limit_ns = g_wait_limit_ns;
   auto kernel = gemm_kernel<MODE, ACT, RES, PRE, CG>;
@@ -189,6 +193,48 @@ int launch_gemm_act(int act, int kid, const GemmPlan& g, const void* a, const vo
     default:
       return launch_gemm<MODE, kActNone>(kid, g, a, b, bias, residual, pre, y, M, N, K, st);
   }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// One or two rows are a read of the weights (1024 -> 4096: 2.9 us for one row,
+// 9.7 on the tensor cores; 4096 -> 4096: 21 us for two, 27); more rows cost
+// this kernel fp32 work in proportion: four of 1024 -> 4096 take 6.0 us (9.9),
+// four of 4096 -> 4096 35.8 us (27.5), eight of 4096 -> 1024 29 us (24).
+bool few_rows_win(int rows, int K, int N) {
+  return rows <= 2 || (rows <= kFewRows && (long long)rows * K * N <= 1ll << 24);
+}
+
+template <int ACT, bool GATED>
+int launch_few_as(int kid, const FewParams& p, cudaStream_t st) {
+  const int per_block = kFewThreads / 32 * (GATED ? 1 : 2);
+  const int grid = div_up(p.N, per_block);
+  TraceScope ts(kid, st);
+  if (p.rows == 1)
+    few_rows_kernel<1, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
+  else if (p.rows == 2)
+    few_rows_kernel<2, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
+  else if (p.rows <= 4)
+    few_rows_kernel<4, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
+  else
+    few_rows_kernel<8, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+template <bool GATED>
+int launch_few(int act, int kid, const void* x, const void* w, const float* bias,
+               const void* residual, void* pre, void* y, int rows, int N, int K, cudaStream_t st) {
+  FewParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.w = static_cast<const __nv_bfloat16*>(w);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.bias = bias;
+  p.pre = static_cast<__nv_bfloat16*>(pre);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.rows = rows; p.K = K; p.N = N;
+  return act == RIB_ACT_GELU   ? launch_few_as<kActGelu, GATED>(kid, p, st)
+         : act == RIB_ACT_SILU ? launch_few_as<kActSilu, GATED>(kid, p, st)
+                               : launch_few_as<kActNone, GATED>(kid, p, st);
 }
 
 struct DwPlan {
@@ -293,15 +339,14 @@ LnPlan plan_ln(int rows, int C, int es, bool bwd, bool aligned, int sms) {
     n.lanes = n.vec == 1 ? 32 : vecs <= 16 ? 4 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
     n.nv = div_up(vecs, n.lanes * (n.vec == 1 ? 2 : 1));
     if (n.vec == 1 || n.nv > 4) n.nv = n.nv <= 4 ? 4 : n.nv <= 8 ? 8 : 16;
-    // A block: whole groups of rows, whole 16 bytes, 32 rows at most (a lane
-    // holds a row's statistics).  Measured at 192 channels of bf16: the forward
+    // A block: whole groups of rows, 32 rows at most (a lane holds a row's
+    // statistics).  Measured at 192 channels of bf16: the forward
     // is best at four rows (1.5 KB; 40.0 us for 294912 rows, 44 at sixteen), the
     // backward at eight (3 KB of each array; 42 us with the sums for 147456
     // rows, 56 at four: its fixed work per block is larger).
-    int unit = 32 / n.lanes;
-    while ((unit * C * es) % 16) unit *= 2;
+    const int unit = n.vec == 1 ? 2 : 32 / n.lanes;   // single elements: two rows interleaved
     n.q.rows = std::min(std::max(1, (bwd ? 9216 : 2048) / (arrays * unit * C * es)) * unit, 32);
-    n.q.bytes = (n.q.rows * C * es + 127) & ~127;
+    n.q.bytes = (n.q.rows * C * es + (n.vec == 1 ? 32 : 0) + 127) & ~127;
     const size_t weights = ((bwd ? 1 : 2) * 4 * C + 127) & ~127;
     for (n.q.stages = kLnMaxStages; n.q.stages >= 2; --n.q.stages) {
       const size_t per_warp = (size_t)n.q.stages * arrays * n.q.bytes + kLnMaxStages * 8;
@@ -605,6 +650,9 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (rows == 0) return RIB_OK;
   if (!x || !w || !y) return RIB_ERR_ARG;
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
+  if (few_rows_win(rows, K, N))
+    return launch_few<false>(act, K_LINEAR, x, w, bias, residual, pre, y, rows, N, K,
+                             static_cast<cudaStream_t>(stream));
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   const GemmPlan g = plan_gemm(kLinear, rows, N, K, residual != nullptr, sms);
@@ -691,6 +739,13 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (few_rows_win(rows, C, 2 * hidden)) {
+    if ((rc = launch_few<true>(act, K_GATED, x, w_in, b_in, nullptr, nullptr, workspace, rows,
+                               hidden, C, st)))
+      return rc;
+    return launch_few<false>(RIB_ACT_NONE, K_LINEAR, workspace, w_out, b_out, residual, nullptr, y,
+                             rows, C, hidden, st);
+  }
   const GemmPlan g = plan_gemm(kGated, rows, hidden, C, false, sms);
   rc = launch_gemm_act<kGated>(act, K_GATED, g, x, w_in, b_in, nullptr, nullptr, workspace, rows,
                                hidden, C, st);

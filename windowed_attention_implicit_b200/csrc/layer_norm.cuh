@@ -568,23 +568,36 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
   const size_t all_bytes = static_cast<size_t>(p.rows) * row_bytes;
   auto rows_of = [&](int b) { return min(q.rows, p.rows - b * q.rows); };
   auto at = [&](int b) { return static_cast<size_t>(b) * (q.rows * row_bytes); };
+  // A block of rows of an odd size begins off a 16-byte address (the tensors
+  // themselves do not): it lies in its stage as it lies in memory, behind the
+  // bytes of the row before it up to the last 16-byte address.
+  auto lead_of = [&](int b) { return V == 1 ? static_cast<uint32_t>(at(b)) & 15u : 0u; };
   auto stage = [&](int s, int a) { return mine + (s * arrays + a) * q.bytes; };
-  // Starts block b's copies into stage s; the up to 15 bytes behind its last
-  // whole 16 (a last block of rows of an odd size only) are copied by the lanes.
+  // Starts block b's copies into stage s, whole 16 bytes; up to 15 bytes that
+  // the tensor has behind its last 16-byte address are copied by the lanes.
   auto load = [&](int b, int s) {
-    const uint32_t bytes = rows_of(b) * row_bytes, whole = V == 1 ? bytes & ~15u : bytes;
-    if (V == 1 && bytes != whole) {
-      for (int a = 0; a < arrays; ++a)
-        if (lane < (bytes - whole) / ES &&
-            rib_guard(at(b) + whole + lane * ES, all_bytes, G_LN_IN))
-          reinterpret_cast<T*>(stage(s, a) + whole)[lane] =
-              reinterpret_cast<const T*>(src[a] + at(b) + whole)[lane];
-      __syncwarp();
-    }
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&full[s], arrays * whole);
-      for (int a = 0; a < arrays && whole; ++a)
-        bulk_load(stage(s, a), src[a] + at(b), whole, &full[s]);
+    const uint32_t bytes = rows_of(b) * row_bytes;
+    if constexpr (V != 1) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], arrays * bytes);
+        for (int a = 0; a < arrays; ++a) bulk_load(stage(s, a), src[a] + at(b), bytes, &full[s]);
+      }
+    } else {
+      const size_t from = at(b) - lead_of(b), end = at(b) + bytes;
+      const size_t to = min((end + 15) & ~static_cast<size_t>(15), all_bytes & ~static_cast<size_t>(15));
+      const uint32_t whole = to > from ? static_cast<uint32_t>(to - from) : 0u;
+      if (from + whole < end) {
+        for (int a = 0; a < arrays; ++a)
+          if (from + whole + lane * ES < end && rib_guard(from + whole + lane * ES, all_bytes, G_LN_IN))
+            reinterpret_cast<T*>(stage(s, a) + whole)[lane] =
+                reinterpret_cast<const T*>(src[a] + from + whole)[lane];
+        __syncwarp();
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], arrays * whole);
+        for (int a = 0; a < arrays && whole; ++a)
+          bulk_load(stage(s, a), src[a] + from, whole, &full[s]);
+      }
     }
   };
   // the rows' statistics, lane r holding row r of the next block
@@ -617,7 +630,8 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
     load_stats(b + step);
     if (!(ok = warp_wait(&full[s], ph, ab, q.wait_limit_ns, SITE_LN))) break;
     const int rows = rows_of(b);
-    uint8_t* x0 = stage(s, 0);
+    const uint32_t lead = lead_of(b);
+    uint8_t* x0 = stage(s, 0) + lead;
     for (int r0 = 0; r0 < rows; r0 += G * RR) {
       uint32_t off[RR];
       bool in_row[RR];
@@ -689,7 +703,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
           }
         }
       } else {
-        uint8_t* d0 = stage(s, 1);
+        uint8_t* d0 = stage(s, 1) + lead;
         float mu[RR], rs[RR], m1[RR], m2[RR];
         uint64_t xc[RR][NV][P], gd[RR][NV][P];   // x - mean, gamma dy
 #pragma unroll
@@ -736,7 +750,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
             if (!in_row[k] || ln_column<V, L>(i, j, 0, 0) >= C) continue;
             uint64_t a[P];
             if (arrays == 3) {
-              LP::get(stage(s, 2) + off[k], i, j, C, a);
+              LP::get(stage(s, 2) + lead + off[k], i, j, C, a);
             } else {
 #pragma unroll
               for (int e = 0; e < P; ++e) a[e] = 0ull;
@@ -752,14 +766,19 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
     fence_proxy_async_smem();
     __syncwarp();
     {
-      const uint8_t* res = stage(s, BWD ? 1 : 0);
-      const uint32_t bytes = rows * row_bytes, whole = V == 1 ? bytes & ~15u : bytes;
-      if (V == 1 && lane < (bytes - whole) / ES &&
-          rib_guard(at(b) + whole + lane * ES, all_bytes, G_LN_OUT))
-        reinterpret_cast<T*>(out + at(b) + whole)[lane] =
-            reinterpret_cast<const T*>(res + whole)[lane];
+      const uint8_t* res = stage(s, BWD ? 1 : 0);   // lies there as byte at(b) - lead does
+      const uint32_t bytes = rows * row_bytes;
+      uint32_t head = 0, whole = bytes;   // bytes before the first 16-byte address; in whole 16s
+      if constexpr (V == 1) {
+        head = min((16u - lead) & 15u, bytes);
+        whole = (bytes - head) & ~15u;
+        const uint32_t edge = lane < 8 ? lane * ES : head + whole + (lane - 8) * ES;
+        if ((lane < 8 ? edge < head : lane < 16 && edge < bytes) &&
+            rib_guard(at(b) + edge, all_bytes, G_LN_OUT))
+          *reinterpret_cast<T*>(out + at(b) + edge) = *reinterpret_cast<const T*>(res + lead + edge);
+      }
       if (lane == 0) {
-        if (whole) bulk_store(out + at(b), res, whole);
+        if (whole) bulk_store(out + at(b) + head, res + lead + head, whole);
         tma_store_commit();
         // the stage that the next copies go to (the block before this one's,
         // or with two stages the one before that) has been read
