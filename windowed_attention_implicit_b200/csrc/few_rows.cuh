@@ -40,6 +40,7 @@ __device__ __forceinline__ void few_unpack(const uint4& r, float (&f)[8]) {
 template <int R, int ACT, bool GATED>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
   constexpr int U = R <= 2 ? 4 : 2;   // 16-byte pieces of each weight row in flight
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int job = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
   const int n0 = GATED ? job : 2 * job;

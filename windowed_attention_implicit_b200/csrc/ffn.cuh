@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     tmem_alloc(&bb.tmem, 512);
     tmem_relinquish();
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -17,6 +17,7 @@
 // 8 (a 16-byte row pitch) run without a special case.
 #pragma once
 
+#include "layer_norm.cuh"   // pdl_wait
 #include "ptx.cuh"
 
 namespace rib {
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (CG == 2) cluster_sync();   // the other CTA's barriers are ready too
   if (warp == kGemmMmaWarp) pair_tmem_alloc<CG>(&bb.tmem, 512);
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -823,6 +825,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     tmem_alloc(&bb.tmem, 512);
     tmem_relinquish();
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -964,6 +967,7 @@ __global__ void __launch_bounds__(256)
     dw_reduce_kernel(const float* part, const float* part_db, int splits, size_t n4, size_t nb4,
                      float* out32, __nv_bfloat16* out16, float* db) {
   __shared__ float4 sums[4][64];
+  pdl_wait();
   const int col = threadIdx.x & 63, group = threadIdx.x >> 6;
   const size_t i = static_cast<size_t>(blockIdx.x) * 64 + col;
   const bool is_db = i >= n4;
@@ -1014,6 +1018,7 @@ struct DzParams {
 template <int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
   __shared__ float sums[8][256];
+  pdl_wait();
   const int oct = threadIdx.x & 31, slot = threadIdx.x >> 5;
   const int c = blockIdx.x * 256 + 8 * oct;
   const size_t n = static_cast<size_t>(p.rows) * p.N;

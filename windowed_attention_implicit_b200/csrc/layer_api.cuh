@@ -15,6 +15,30 @@
 namespace rib {
 namespace {
 
+// ---------------------------------------------------------------- launches
+
+// Launches a kernel that calls pdl_wait(), optionally in clusters.
+template <typename... Args>
+int launch(void (*kernel)(Args...), dim3 grid, int block, size_t smem, cudaStream_t st, int cluster,
+           Args... args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return RIB_OK;
+  cudaGetLastError();
+  return RIB_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- shapes
 
 constexpr int kMaxChannels = 65536;
@@ -138,26 +162,7 @@ int launch_gemm_as(int kid, const GemmPlan& g, const void* a, const void* b, con
   auto kernel = gemm_kernel<MODE, ACT, RES, PRE, CG>;
   if ((rc = set_smem(kernel, g.smem))) return rc;
   TraceScope ts(kid, st);
-  if constexpr (CG == 1) {
-    kernel<<<g.grid, kGemmThreads, g.smem, st>>>(ta, tb, ty, tp, tr, p);
-  } else {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(g.grid);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = g.smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, tp, tr, p) != cudaSuccess) {
-      cudaGetLastError();
-      return RIB_ERR_CUDA;
-    }
-  }
-  return launch_status();
+  return launch(kernel, dim3(g.grid), kGemmThreads, g.smem, st, CG, ta, tb, ty, tp, tr, p);
 }
 
 // The epilogue's optional reads and writes are template arguments: an absent
@@ -211,14 +216,12 @@ int launch_few_as(int kid, const FewParams& p, cudaStream_t st) {
   const int grid = div_up(p.N, per_block);
   TraceScope ts(kid, st);
   if (p.rows == 1)
-    few_rows_kernel<1, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
-  else if (p.rows == 2)
-    few_rows_kernel<2, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
-  else if (p.rows <= 4)
-    few_rows_kernel<4, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
-  else
-    few_rows_kernel<8, ACT, GATED><<<grid, kFewThreads, 0, st>>>(p);
-  return launch_status();
+    return launch(few_rows_kernel<1, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
+  if (p.rows == 2)
+    return launch(few_rows_kernel<2, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
+  if (p.rows <= 4)
+    return launch(few_rows_kernel<4, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
+  return launch(few_rows_kernel<8, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
 }
 
 template <bool GATED>
@@ -298,16 +301,23 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   if ((rc = set_smem(dw_kernel, smem))) return rc;
   {
     TraceScope ts(K_DW, st);
-    dw_kernel<<<d.m_tiles * d.n_tiles * d.splits, kDwThreads, smem, st>>>(tz, tx, p);
-    if ((rc = launch_status())) return rc;
+    rc = launch(dw_kernel, dim3(d.m_tiles * d.n_tiles * d.splits), kDwThreads, smem, st, 1, tz, tx, p);
+    if (rc) return rc;
   }
   if (direct) return rc;
   TraceScope ts(K_DW_RED, st);
   const size_t n4 = (size_t)N * K / 4, nb4 = db ? N / 4 : 0;
-  dw_reduce_kernel<<<div_up((long long)(n4 + nb4), 64), 256, 0, st>>>(
-      p.part, p.part_db, d.splits, n4, nb4, f32 ? static_cast<float*>(dw) : nullptr,
-      f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db);
-  return launch_status();
+  return launch(dw_reduce_kernel, dim3(div_up((long long)(n4 + nb4), 64)), 256, 0, st, 1,
+                static_cast<const float*>(p.part), static_cast<const float*>(p.part_db), d.splits,
+                n4, nb4, f32 ? static_cast<float*>(dw) : nullptr,
+                f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db);
+}
+
+int launch_reduce_rows(const float* part, int rows, int n0, float* out0, int n1, float* out1,
+                       cudaStream_t st) {
+  TraceScope ts(K_ROWS_RED, st);
+  return launch(reduce_rows_kernel, dim3(div_up(n0 + n1, 32)), kLnThreads, 0, st, 1, part, rows,
+                n0, out0, n1, out1);
 }
 
 bool aligned16_all(std::initializer_list<const void*> ptrs) {
@@ -377,15 +387,13 @@ template <typename T, int V, int NV, bool CTA>
 int ln_launch_row(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
   if (!bwd) {
     TraceScope ts(K_LN_FWD, st);
-    ln_row_fwd_kernel<T, V, NV, CTA><<<n.grid, kLnThreads, 0, st>>>(p);
-    return launch_status();
+    return launch(ln_row_fwd_kernel<T, V, NV, CTA>, dim3(n.grid), kLnThreads, 0, st, 1, p);
   }
   const size_t smem = CTA || !p.part ? 0 : (size_t)kLnWarps * 2 * p.C * 4;
   int rc = set_smem(ln_row_bwd_kernel<T, V, NV, CTA>, smem);
   if (rc) return rc;
   TraceScope ts(K_LN_BWD, st);
-  ln_row_bwd_kernel<T, V, NV, CTA><<<n.grid, kLnThreads, smem, st>>>(p);
-  return launch_status();
+  return launch(ln_row_bwd_kernel<T, V, NV, CTA>, dim3(n.grid), kLnThreads, smem, st, 1, p);
 }
 
 template <typename T, int V, int NV, int L>
@@ -396,8 +404,7 @@ int ln_launch_async(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t s
   LnBlocks q = n.q;
   q.wait_limit_ns = g_wait_limit_ns;
   TraceScope ts(bwd ? K_LN_BWD : K_LN_FWD, st);
-  kernel<<<n.grid, 32 * q.warps, n.smem, st>>>(p, q);
-  return launch_status();
+  return launch(kernel, dim3(n.grid), 32 * q.warps, n.smem, st, 1, p, q);
 }
 
 template <typename T>
@@ -542,8 +549,7 @@ size_t dtype_bytes(int dtype) { return dtype == RIB_DTYPE_F32 ? 4 : 2; }
 template <int ACT>
 int launch_dz(const DzParams& p, int row_splits, cudaStream_t st) {
   TraceScope ts(K_DZ, st);
-  dz_kernel<ACT><<<dim3(div_up(p.N, 256), row_splits), 256, 0, st>>>(p);
-  return launch_status();
+  return launch(dz_kernel<ACT>, dim3(div_up(p.N, 256), row_splits), 256, 0, st, 1, p);
 }
 
 template <int ACT>
@@ -565,8 +571,8 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
   if (rc) return rc;
   if ((rc = set_smem(ffn_bwd_kernel<ACT>, w.f.smem))) return rc;
   TraceScope ts(K_FFN_BWD, st);
-  ffn_bwd_kernel<ACT><<<w.f.grid, kFfnThreads, w.f.smem, st>>>(tx, ty, ti, to, th, td, p);
-  return launch_status();
+  return launch(ffn_bwd_kernel<ACT>, dim3(w.f.grid), kFfnThreads, w.f.smem, st, 1, tx, ty, ti, to,
+                th, td, p);
 }
 
 }  // namespace
@@ -637,10 +643,7 @@ int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C
   rc = dtype == RIB_DTYPE_BF16 ? ln_dispatch<__nv_bfloat16>(p, n, true, st)
                                : ln_dispatch<float>(p, n, true, st);
   if (rc || !sums) return rc;
-  TraceScope ts(K_ROWS_RED, st);
-  reduce_rows_kernel<<<div_up(2 * C, 32), kLnThreads, 0, st>>>(p.part, n.grid, C, dgamma, C,
-                                                               dbeta);
-  return launch_status();
+  return launch_reduce_rows(p.part, n.grid, C, dgamma, C, dbeta, st);
 }
 
 int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const float* bias,
@@ -701,10 +704,7 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     if (rc) return rc;
     if (act != RIB_ACT_NONE) dz = p.dz;
     if (db) {
-      TraceScope ts(K_ROWS_RED, st);
-      reduce_rows_kernel<<<div_up(N, 32), kLnThreads, 0, st>>>(p.part, L.row_splits, N, db, 0,
-                                                               nullptr);
-      if ((rc = launch_status())) return rc;
+      if ((rc = launch_reduce_rows(p.part, L.row_splits, N, db, 0, nullptr, st))) return rc;
     }
   }
   if (dx) {
@@ -798,10 +798,8 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
                              : launch_ffn_bwd<kActNone>(L, x, dy, w_in, w_out, p, ws, st);
   if (rc) return rc;
   if (db_in) {
-    TraceScope ts(K_ROWS_RED, st);
-    reduce_rows_kernel<<<div_up(2 * hidden, 32), kLnThreads, 0, st>>>(
-        p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr);
-    if ((rc = launch_status())) return rc;
+    if ((rc = launch_reduce_rows(p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr, st)))
+      return rc;
   }
   const GemmPlan g = plan_gemm(kDx, rows, C, 2 * hidden, dx_add != nullptr, sms);
   rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, ws + L.d, w_in, nullptr, dx_add, nullptr, dx,

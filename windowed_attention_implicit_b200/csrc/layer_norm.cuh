@@ -35,6 +35,16 @@ constexpr int kLnWarps = kLnThreads / 32;
 constexpr int kLnMaxC = 8192;
 constexpr int G_LN_IN = 160, G_LN_OUT = 161, G_LN_STAT = 162, G_LN_PART = 163;
 
+// Programmatic dependent launch: a kernel lets the next one's blocks start as
+// soon as SMs are free (at its own start: these kernels fill the SMs in one
+// wave), and each kernel waits for the one before it, complete with its
+// writes, before it touches global memory.  Only launch latency and a
+// kernel's set-up overlap the one before.  Every block of a kernel launched
+// this way calls it, so that kernels stay ordered one after the other.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+
 struct LnParams {
   const void* x;
   const void* dy;
@@ -160,6 +170,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_row_fwd_kernel(const LnParams p
   constexpr int R = ln_rows<V, NV, CTA>();
   constexpr int G = CTA ? kLnThreads : 32;
   __shared__ float buf[2][kLnWarps];
+  pdl_wait();
   const int t = CTA ? threadIdx.x : threadIdx.x & 31;
   const int C = p.C;
   const size_t elems = static_cast<size_t>(p.rows) * C;
@@ -255,6 +266,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_row_bwd_kernel(const LnParams p
   constexpr int G = CTA ? kLnThreads : 32;
   __shared__ float buf[2][2][kLnWarps];
   extern __shared__ float ln_sums[];
+  pdl_wait();
   const int t = CTA ? threadIdx.x : threadIdx.x & 31;
   const int C = p.C;
   const size_t elems = static_cast<size_t>(p.rows) * C;
@@ -553,6 +565,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
     for (int i = 0; i < q.stages; ++i) mbar_init(&full[i], 1);
     fence_mbarrier_init();
   }
+  pdl_wait();
   for (int c = threadIdx.x; c < C; c += blockDim.x) {
     s_gamma[ln_weight_slot<V>(c, C)] = p.gamma ? __ldg(p.gamma + c) : 1.f;
     if (!BWD) s_beta[ln_weight_slot<V>(c, C)] = p.beta ? __ldg(p.beta + c) : 0.f;
@@ -846,6 +859,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
 __global__ void __launch_bounds__(kLnThreads)
     reduce_rows_kernel(const float* part, int rows, int n0, float* out0, int n1, float* out1) {
   __shared__ float sums[kLnWarps][32];
+  pdl_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = n0 + n1, c = blockIdx.x * 32 + lane;
   const size_t total = static_cast<size_t>(rows) * n;
