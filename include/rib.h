@@ -469,9 +469,10 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
  *   w_out  : bf16 [C][hidden];                 b_out : fp32 [C] or NULL
  *   residual : bf16 [rows][C] or NULL
  *   y      : out, bf16 [rows][C]; may be residual
- *   workspace : device, >= rib_gated_ffn_fwd_workspace() bytes (h in bf16, as
- *            the second product takes it), 256-byte aligned
- * hidden <= 32768.
+ *   workspace : device, >= rib_gated_ffn_fwd_workspace() bytes (h, where two
+ *            products are faster than one kernel; 0: may be NULL) on the current
+ *            device, 256-byte aligned
+ * h is rounded to bf16, as the second product takes it; y once.  hidden <= 32768.
  * ------------------------------------------------------------------------ */
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden);
 int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_in,

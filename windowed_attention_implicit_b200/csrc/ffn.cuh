@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   uint8_t* s_stage = s_res + (p.b_resident ? p.k_steps * kFfnB : 0u);
   FfnBars& bb = *reinterpret_cast<FfnBars*>(s_stage + kFfnStaging);
   volatile int* ab = &bb.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int items = p.n_tiles * p.splits;
   const uint64_t lim = p.wait_limit_ns;
   if (threadIdx.x == 0) {

@@ -11,6 +11,7 @@
 #include "gemm.cuh"
 #include "ffn.cuh"
 #include "few_rows.cuh"
+#include "ffn_fused.cuh"
 
 namespace rib {
 namespace {
@@ -211,10 +212,10 @@ bool few_rows_win(int rows, int K, int N) {
 }
 
 template <int ACT, bool GATED>
-int launch_few_as(int kid, const FewParams& p, cudaStream_t st) {
+int launch_few_as(const FewParams& p, cudaStream_t st) {
   const int per_block = kFewThreads / 32 * (GATED ? 1 : 2);
   const int grid = div_up(p.N, per_block);
-  TraceScope ts(kid, st);
+  TraceScope ts(K_FEW_ROWS, st);
   if (p.rows == 1)
     return launch(few_rows_kernel<1, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
   if (p.rows == 2)
@@ -225,8 +226,8 @@ int launch_few_as(int kid, const FewParams& p, cudaStream_t st) {
 }
 
 template <bool GATED>
-int launch_few(int act, int kid, const void* x, const void* w, const float* bias,
-               const void* residual, void* pre, void* y, int rows, int N, int K, cudaStream_t st) {
+int launch_few(int act, const void* x, const void* w, const float* bias, const void* residual,
+               void* pre, void* y, int rows, int N, int K, cudaStream_t st) {
   FewParams p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.w = static_cast<const __nv_bfloat16*>(w);
@@ -235,9 +236,9 @@ int launch_few(int act, int kid, const void* x, const void* w, const float* bias
   p.pre = static_cast<__nv_bfloat16*>(pre);
   p.y = static_cast<__nv_bfloat16*>(y);
   p.rows = rows; p.K = K; p.N = N;
-  return act == RIB_ACT_GELU   ? launch_few_as<kActGelu, GATED>(kid, p, st)
-         : act == RIB_ACT_SILU ? launch_few_as<kActSilu, GATED>(kid, p, st)
-                               : launch_few_as<kActNone, GATED>(kid, p, st);
+  return act == RIB_ACT_GELU   ? launch_few_as<kActGelu, GATED>(p, st)
+         : act == RIB_ACT_SILU ? launch_few_as<kActSilu, GATED>(p, st)
+                               : launch_few_as<kActNone, GATED>(p, st);
 }
 
 struct DwPlan {
@@ -575,6 +576,59 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
                 th, td, p);
 }
 
+// ---------------------------------------------------------------- fused feed-forward
+
+// A pair takes the same time for a row tile however few tiles there are, and
+// the two products spread few rows over more SMs: one kernel wins from a tile
+// per pair on (147456 rows, silu, residual: 192 x 384 92 us for 92, 192 x 768
+// 154 for 159, 96 x 384 74 for 83; 65536 x 256 x 1024 111 for 116; without a
+// residual 81 for 82, 138 for 149, 65 for 79, 98 for 121; at worst, 149 tiles on
+// 74 pairs, 58 for 52), below that where a tile is short (4096 x 96 x 192 8.9 for
+// 9.8; 9216 x 192 x 384 15 for 16; 8192 x 128 x 512 15.9 for 16.1; but 4096 x 128 x
+// 512 15.5 for 13.5, 8192 x 256 x 1024 30 for 24.5).
+bool fused_wins(int rows, int C, int hidden, int sms) {
+  const int tiles = div_up(rows, 256);
+  return C <= kFusedMaxC && (tiles >= sms / 2 || tiles >= 3 * div_up(hidden, 64));
+}
+
+template <int ACT, bool RES>
+int launch_fused_as(const void* x, const void* w_in, const float* b_in, const void* w_out,
+                    const float* b_out, const void* residual, void* y, int rows, int C, int H,
+                    int sms, cudaStream_t st) {
+  CUtensorMap tx, ti, to, ty, tr;
+  int rc = map_2d(&tx, x, rows, C, 64, 128);
+  if (!rc) rc = map_2d(&ti, w_in, 2ull * H, C, 64, 64);
+  if (!rc) rc = map_2d(&to, w_out, C, H, 64, fused_cols(C) / 2);
+  if (!rc) rc = map_2d(&ty, y, rows, C, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!rc) rc = map_2d(&tr, RES ? residual : y, rows, C, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (rc) return rc;
+  FusedParams p{};
+  p.b_in = b_in; p.b_out = b_out;
+  p.M = rows; p.C = C; p.H = H;
+  p.m_tiles = div_up(rows, 256);
+  p.chunks = div_up(H, 64);
+  p.k_steps = div_up(C, 64);
+  p.ring = kFusedMaxRing;
+  while (p.ring > 2 && fused_smem_bytes(C, p.ring) > kSmemMax) --p.ring;
+  p.wait_limit_ns = g_wait_limit_ns;
+  const size_t smem = fused_smem_bytes(C, p.ring);
+  auto kernel = ffn_fused_kernel<ACT, RES>;
+  if ((rc = set_smem(kernel, smem))) return rc;
+  TraceScope ts(K_FFN_FUSED, st);
+  return launch(kernel, dim3(2 * std::min(p.m_tiles, sms / 2)), kGemmThreads, smem, st, 2, tx, ti,
+                to, ty, tr, p);
+}
+
+template <int ACT>
+int launch_fused(const void* x, const void* w_in, const float* b_in, const void* w_out,
+                 const float* b_out, const void* residual, void* y, int rows, int C, int H,
+                 int sms, cudaStream_t st) {
+  return residual ? launch_fused_as<ACT, true>(x, w_in, b_in, w_out, b_out, residual, y, rows, C,
+                                               H, sms, st)
+                  : launch_fused_as<ACT, false>(x, w_in, b_in, w_out, b_out, residual, y, rows, C,
+                                                H, sms, st);
+}
+
 }  // namespace
 }  // namespace rib
 
@@ -654,7 +708,7 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (!x || !w || !y) return RIB_ERR_ARG;
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
   if (few_rows_win(rows, K, N))
-    return launch_few<false>(act, K_LINEAR, x, w, bias, residual, pre, y, rows, N, K,
+    return launch_few<false>(act, x, w, bias, residual, pre, y, rows, N, K,
                              static_cast<cudaStream_t>(stream));
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
@@ -720,7 +774,11 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
 }
 
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden) {
+  int sms = 0;
   if (check_ffn(rows, C, hidden)) return 0;
+  if (device_sms(&sms) == RIB_OK && !few_rows_win(rows, C, 2 * hidden) &&
+      fused_wins(rows, C, hidden, sms))
+    return 0;
   return align256((size_t)rows * hidden * 2);
 }
 
@@ -740,12 +798,19 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows_win(rows, C, 2 * hidden)) {
-    if ((rc = launch_few<true>(act, K_GATED, x, w_in, b_in, nullptr, nullptr, workspace, rows,
+    if ((rc = launch_few<true>(act, x, w_in, b_in, nullptr, nullptr, workspace, rows,
                                hidden, C, st)))
       return rc;
-    return launch_few<false>(RIB_ACT_NONE, K_LINEAR, workspace, w_out, b_out, residual, nullptr, y,
+    return launch_few<false>(RIB_ACT_NONE, workspace, w_out, b_out, residual, nullptr, y,
                              rows, C, hidden, st);
   }
+  if (fused_wins(rows, C, hidden, sms))
+    return act == RIB_ACT_GELU   ? launch_fused<kActGelu>(x, w_in, b_in, w_out, b_out, residual, y,
+                                                          rows, C, hidden, sms, st)
+           : act == RIB_ACT_SILU ? launch_fused<kActSilu>(x, w_in, b_in, w_out, b_out, residual, y,
+                                                          rows, C, hidden, sms, st)
+                                 : launch_fused<kActNone>(x, w_in, b_in, w_out, b_out, residual, y,
+                                                          rows, C, hidden, sms, st);
   const GemmPlan g = plan_gemm(kGated, rows, hidden, C, false, sms);
   rc = launch_gemm_act<kGated>(act, K_GATED, g, x, w_in, b_in, nullptr, nullptr, workspace, rows,
                                hidden, C, st);

@@ -9,6 +9,8 @@
   X(K_LINEAR, "gemm_kernel (linear)")       \
   X(K_LINEAR_DX, "gemm_kernel (dx)")        \
   X(K_GATED, "gemm_kernel (gated)")         \
+  X(K_FFN_FUSED, "ffn_fused_kernel")        \
+  X(K_FEW_ROWS, "few_rows_kernel")          \
   X(K_DZ, "dz_kernel")                      \
   X(K_DW, "dw_kernel")                      \
   X(K_DW_RED, "dw_reduce_kernel")           \
