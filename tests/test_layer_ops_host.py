@@ -187,3 +187,18 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
     with pytest.raises(R.RibError, match="current device is cuda:0") as e:
         R._Call("rib_linear_fwd", Elsewhere(), None)
     assert e.value.code == ARG
+
+
+def test_block_weight_gradients_share_one_buffer():
+    from windowed_attention_implicit_b200.parallel import FlatGrads
+    from windowed_attention_implicit_b200.schedule import BlockWeights
+    C, Hd = 16, 24
+    z = torch.zeros
+    ffn = R.GatedFfn.from_params(z(2, Hd, C), z(2, Hd), z(C, Hd), None, device="cpu")
+    w = BlockWeights(z(C), z(C), z(3 * C, C), None, z(C, C), z(C), z(C), z(C), ffn)
+    g = FlatGrads.for_block(w).named()
+    assert "b_qkv" not in g and "b_out" not in g and g["w_in"].shape == (2, Hd, C)
+    assert sum(t.numel() for t in g.values()) == 3 * C * C + C * C + 5 * C + 2 * Hd * C + 2 * Hd + C * Hd
+    base = g["norm1_gamma"].data_ptr()
+    # at the 16-byte addresses that the projections' gradients need
+    assert all((g[n].data_ptr() - base) % 16 == 0 for n in ("w_qkv", "w_proj", "w_in", "w_out", "b_in"))

@@ -31,7 +31,8 @@ def shard_batch(global_batch: int, world: int, rank: int) -> slice:
 class FlatGrads:
     """Gradients as views of one contiguous buffer, so that the cross-rank
     sum is a single all-reduce.  Layouts: the position MLPs (`for_mlp`), the
-    CLA gate (`for_cla`), or both (`for_mlp_and_cla`, MLP first)."""
+    CLA gate (`for_cla`), both (`for_mlp_and_cla`, MLP first), or a block's
+    norms, projections and feed-forward weights (`for_block`)."""
 
     ORDER = ("q_dw1", "q_db1", "q_dw2", "q_db2", "k_dw1", "k_db1", "k_dw2", "k_db2")
     CLA_ORDER = ("cla_dw_dw", "cla_db_dw", "cla_dw_pw", "cla_db_pw")
@@ -77,6 +78,13 @@ class FlatGrads:
     def for_mlp_and_cla(cls, mlp: PositionMLP, channels: int) -> "FlatGrads":
         return cls(cls._mlp_shapes(mlp) + cls._cla_shapes(channels), mlp.q_w1.device,
                    names=cls.ORDER + cls.CLA_ORDER)
+
+    @classmethod
+    def for_block(cls, weights) -> "FlatGrads":
+        """The weight gradients of schedule.BlockWeights; `named()` is what
+        RIBBlock.backward takes as grads."""
+        shapes = weights.grad_shapes()
+        return cls(list(shapes.values()), weights.w_qkv.device, names=tuple(shapes))
 
     def as_grad(self) -> PositionMLPGrad:
         """The position-MLP views as the binding's gradient record."""
