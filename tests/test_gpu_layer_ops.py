@@ -207,7 +207,11 @@ def test_layer_norm_nan_and_inf_stay_in_their_row(dtype, C):
 
 LINEAR = [(1, 8, 8), (1, 192, 576), (2, 16, 24), (127, 96, 96), (128, 64, 64), (129, 72, 200),
           (257, 192, 576), (300, 520, 264), (1000, 1032, 40), (64, 8, 1032), (513, 264, 2056),
-          (38401, 72, 72), (20000, 1032, 64), (40000, 16, 520)]
+          (38401, 72, 72), (20000, 1032, 64), (40000, 16, 520),
+          # few rows (without the tensor cores up to a size), part of a row tile,
+          # weight gradients in tiles of 128, 192 and 256 rows
+          (3, 96, 288), (4, 4096, 40), (5, 1024, 2048), (7, 256, 72), (8, 64, 4096), (6, 2048, 2056),
+          (9, 192, 576), (33, 128, 256), (256, 64, 16), (5000, 192, 192), (4097, 256, 320)]
 
 
 def _linear_case(rows, K, N, seed=21):
@@ -327,7 +331,11 @@ def test_linear_non_finite_rows_stay_apart():
 # ------------------------------------------------------------------ gated feed-forward
 
 FFN = [(1, 8, 8), (5, 16, 24), (129, 96, 192), (130, 72, 200), (400, 264, 520), (300, 192, 384),
-       (30000, 64, 64), (12000, 520, 72), (1, 192, 1032)]
+       (30000, 64, 64), (12000, 520, 72), (1, 192, 1032), (3, 64, 128), (8, 32, 64), (17, 64, 2816),
+       # in one kernel: short and ragged row tiles, channels and hidden channels,
+       # one to three tiles a CTA pair
+       (257, 256, 8), (769, 200, 56), (2000, 72, 128), (2560, 136, 192), (19300, 40, 200),
+       (40000, 256, 72), (25000, 16, 344)]
 
 
 def _ffn_case(rows, C, Hd, seed=41):
@@ -408,8 +416,24 @@ def test_gated_ffn_backward(rows, C, Hd, act):
             _within(out["db_out"], dbo, (2 * rows + 300) * U * D.sum(0), "db_out")
 
 
-def test_gated_ffn_outputs_may_take_their_residuals_place():
-    x, wi, bi, wo, bo, r = _ffn_case(700, 96, 192)
+@pytest.mark.parametrize("rows,C,Hd", [(6, 64, 96), (800, 96, 64), (300, 192, 384)])
+def test_gated_ffn_non_finite_rows_stay_apart(rows, C, Hd):
+    x, wi, bi, wo, bo, r = _ffn_case(rows, C, Hd)
+    ffn = _ffn_dev(wi, bi, wo, bo)
+    clean = R.rib_gated_ffn_fwd(x.cuda(), ffn, residual=r.cuda())
+    x[2, 7], x[rows - 1, 0], r[1, 3] = float("nan"), float("inf"), float("inf")
+    y = R.rib_gated_ffn_fwd(x.cuda(), ffn, residual=r.cuda())
+    _done()
+    rest = [i for i in range(rows) if i not in (1, 2, rows - 1)]
+    assert torch.equal(y[rest], clean[rest]) and torch.isnan(y[2]).all()
+    assert not torch.isfinite(y[rows - 1]).any() and torch.isinf(y[1, 3])
+    cols = [c for c in range(C) if c != 3]
+    assert torch.equal(y[1, cols], clean[1, cols])
+
+
+@pytest.mark.parametrize("Hd", [192, 64])
+def test_gated_ffn_outputs_may_take_their_residuals_place(Hd):
+    x, wi, bi, wo, bo, r = _ffn_case(700 if Hd > 64 else 800, 96, Hd)
     ffn = _ffn_dev(wi, bi, wo, bo)
     x, r = x.cuda(), r.cuda()
     y = R.rib_gated_ffn_fwd(x, ffn, residual=r)
@@ -431,6 +455,8 @@ def _calls(rows=600, C=96, Hd=200, seed=61):
     dw_, pre = _rand((rows, Hd), seed + 5).cuda(), _rand((rows, Hd), seed + 6).cuda()
     _, wi, bi, wo, bo, _ = _ffn_case(1, C, Hd, seed + 7)
     ffn = _ffn_dev(wi, bi, wo, bo)
+    _, wi, bi, wo, bo, _ = _ffn_case(1, C, 64, seed + 8)
+    thin = _ffn_dev(wi, bi, wo, bo)
     _, mean, rstd = R.rib_layer_norm_fwd(x)
     rc, rh, cc, hh = ((rows, C), bf), ((rows, Hd), bf), ((C,), f32), ((Hd,), f32)
     return {
@@ -445,13 +471,15 @@ def _calls(rows=600, C=96, Hd=200, seed=61):
         "linear_bwd_plain": (lambda o, **k: R.rib_linear_bwd(x, w, dw_, dx=o[0], dw=o[1], db=o[2], **k),
                              [rc, ((Hd, C), f32), hh]),
         "ffn_fwd": (lambda o, **k: R.rib_gated_ffn_fwd(x, ffn, residual=dy, y=o[0], **k), [rc]),
+        "ffn_fwd_one_kernel": (lambda o, **k: R.rib_gated_ffn_fwd(x, thin, residual=dy, y=o[0], **k), [rc]),
         "ffn_bwd": (lambda o, **k: R.rib_gated_ffn_bwd(x, ffn, dy, dx=o[0], dw_in=o[1], db_in=o[2], dw_out=o[3],
                                                        db_out=o[4], **k),
                     [rc, ((2, Hd, C), f32), ((2, Hd), f32), ((C, Hd), f32), cc]),
     }
 
 
-NAMES = ["norm_fwd", "norm_bwd", "linear_fwd", "linear_bwd", "linear_bwd_plain", "ffn_fwd", "ffn_bwd"]
+NAMES = ["norm_fwd", "norm_bwd", "linear_fwd", "linear_bwd", "linear_bwd_plain", "ffn_fwd",
+         "ffn_fwd_one_kernel", "ffn_bwd"]
 
 
 def _fresh(spec):
