@@ -968,22 +968,27 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
 }
 
-// dW and db = the sums of the splits' partials: four groups of threads take a
-// quarter of the splits each, in order, and their sums are added in order.
-// n4 = N K / 4 float4 of dW (none when there is one split), then N / 4 of db;
-// dW fp32 or rounded to bf16 once.  grid ceil((n4 + nb4) / 64), block 256.
+// db and dW = the sums of their partials.  Groups of threads take a run of the
+// partials each, in order, and the groups' sums are added in order: for db,
+// whose partials may be another kernel's and many more, sixteen groups (in the
+// first db_blocks blocks), for dW four.  nb4 = N / 4 float4 of db, n4 = N K / 4
+// of dW (none when there is one split); dW fp32 or rounded to bf16 once.
+// grid db_blocks + ceil(n4 / 64), db_blocks = ceil(nb4 / 16), block 256.
 __global__ void __launch_bounds__(256)
-    dw_reduce_kernel(const float* part, const float* part_db, int splits, size_t n4, size_t nb4,
-                     float* out32, __nv_bfloat16* out16, float* db) {
-  __shared__ float4 sums[4][64];
+    dw_reduce_kernel(const float* part, const float* part_db, int dw_splits, int db_splits,
+                     size_t n4, size_t nb4, float* out32, __nv_bfloat16* out16, float* db) {
+  __shared__ float4 sums[256];
   pdl_wait();
-  const int col = threadIdx.x & 63, group = threadIdx.x >> 6;
-  const size_t i = static_cast<size_t>(blockIdx.x) * 64 + col;
-  const bool is_db = i >= n4;
+  const unsigned db_blocks = static_cast<unsigned>((nb4 + 15) / 16);
+  const bool is_db = blockIdx.x < db_blocks;
+  const int cols = is_db ? 16 : 64, groups = 256 / cols;
+  const int col = threadIdx.x % cols, group = threadIdx.x / cols;
+  const size_t i = static_cast<size_t>(blockIdx.x - (is_db ? 0u : db_blocks)) * cols + col;
   const float* src = is_db ? part_db : part;
-  const size_t n = 4 * (is_db ? nb4 : n4), at0 = 4 * (is_db ? i - n4 : i);
-  const bool in = i < n4 + nb4;
-  const int per = (splits + 3) / 4, k1 = min(splits, (group + 1) * per);
+  const int splits = is_db ? db_splits : dw_splits;
+  const size_t n = 4 * (is_db ? nb4 : n4), at0 = 4 * i;
+  const bool in = at0 < n;
+  const int per = (splits + groups - 1) / groups, k1 = min(splits, (group + 1) * per);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (in) {
 #pragma unroll 4
@@ -994,12 +999,11 @@ __global__ void __launch_bounds__(256)
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
   }
-  sums[group][col] = s;
+  sums[threadIdx.x] = s;
   __syncthreads();
   if (group != 0 || !in) return;
-#pragma unroll
-  for (int g = 1; g < 4; ++g) {
-    const float4 v = sums[g][col];
+  for (int g = 1; g < groups; ++g) {
+    const float4 v = sums[g * cols + col];
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
   if (is_db)

@@ -282,8 +282,17 @@ DwPlan plan_dw(int rows, int N, int K, int sms) {
 }
 
 // dW = dz^T x (fp32, or bf16) and, with db, its column sums.
+int launch_dw_reduce(const float* part, int splits, size_t n4, const float* part_db, int db_splits,
+                     size_t nb4, float* out32, __nv_bfloat16* out16, float* db, cudaStream_t st) {
+  TraceScope ts(K_DW_RED, st);
+  return launch(dw_reduce_kernel, dim3(div_up(nb4, 16) + div_up(n4, 64)), 256, 0, st, 1, part,
+                part_db, splits, db_splits, n4, nb4, out32, out16, db);
+}
+
+// db_rows: the partials of db that part_db holds already, or 0: the product
+// forms them
 int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, int K, void* dw,
-              int dw_dtype, float* db, void* part, void* part_db, cudaStream_t st) {
+              int dw_dtype, float* db, void* part, void* part_db, int db_rows, cudaStream_t st) {
   CUtensorMap tz, tx;
   int rc = map_2d(&tz, dz, rows, N, 64, 64);
   if (!rc) rc = map_2d(&tx, x, rows, K, 64, 64);
@@ -296,7 +305,7 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   p.steps = d.steps; p.steps_per_split = d.per_split;
   p.part = static_cast<float*>(direct ? (f32 ? dw : nullptr) : part);
   p.out16 = direct && !f32 ? static_cast<__nv_bfloat16*>(dw) : nullptr;
-  p.part_db = !db ? nullptr : direct ? db : static_cast<float*>(part_db);
+  p.part_db = !db || db_rows ? nullptr : direct ? db : static_cast<float*>(part_db);
   p.wait_limit_ns = g_wait_limit_ns;
   const size_t smem = dw_smem_bytes(d.a_chunks, d.b_chunks, d.stages);
   if ((rc = set_smem(dw_kernel, smem))) return rc;
@@ -305,13 +314,11 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
     rc = launch(dw_kernel, dim3(d.m_tiles * d.n_tiles * d.splits), kDwThreads, smem, st, 1, tz, tx, p);
     if (rc) return rc;
   }
-  if (direct) return rc;
-  TraceScope ts(K_DW_RED, st);
-  const size_t n4 = (size_t)N * K / 4, nb4 = db ? N / 4 : 0;
-  return launch(dw_reduce_kernel, dim3(div_up((long long)(n4 + nb4), 64)), 256, 0, st, 1,
-                static_cast<const float*>(p.part), static_cast<const float*>(p.part_db), d.splits,
-                n4, nb4, f32 ? static_cast<float*>(dw) : nullptr,
-                f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db);
+  const size_t n4 = direct ? 0 : (size_t)N * K / 4, nb4 = db && (db_rows || !direct) ? N / 4 : 0;
+  if (n4 + nb4 == 0) return rc;
+  return launch_dw_reduce(p.part, d.splits, n4, static_cast<const float*>(part_db),
+                          db_rows ? db_rows : d.splits, nb4, f32 ? static_cast<float*>(dw) : nullptr,
+                          f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db, st);
 }
 
 int launch_reduce_rows(const float* part, int rows, int n0, float* out0, int n1, float* out1,
@@ -757,9 +764,10 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
                                : launch_dz<kActNone>(p, L.row_splits, st);
     if (rc) return rc;
     if (act != RIB_ACT_NONE) dz = p.dz;
-    if (db) {
-      if ((rc = launch_reduce_rows(p.part, L.row_splits, N, db, 0, nullptr, st))) return rc;
-    }
+    if (db && !dw)   // with dW they are added in its reduction
+      if ((rc = launch_dw_reduce(nullptr, 0, 0, p.part, L.row_splits, N / 4, nullptr, nullptr, db,
+                                 st)))
+        return rc;
   }
   if (dx) {
     const GemmPlan g = plan_gemm(kDx, rows, K, N, dx_add != nullptr, sms);
@@ -768,8 +776,8 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     if (rc) return rc;
   }
   if (dw)
-    rc = launch_dw(L.dw, dz, x, rows, N, K, dw, dw_dtype, db_in_dw ? db : nullptr, ws + L.part_dw,
-                   ws + L.part_db, st);
+    rc = launch_dw(L.dw, dz, x, rows, N, K, dw, dw_dtype, db, ws + L.part_dw,
+                   ws + (db_in_dw ? L.part_db : L.part_sum), db_in_dw ? 0 : L.row_splits, st);
   return rc;
 }
 
@@ -862,19 +870,15 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
        : act == RIB_ACT_SILU ? launch_ffn_bwd<kActSilu>(L, x, dy, w_in, w_out, p, ws, st)
                              : launch_ffn_bwd<kActNone>(L, x, dy, w_in, w_out, p, ws, st);
   if (rc) return rc;
-  if (db_in) {
-    if ((rc = launch_reduce_rows(p.part, L.f.splits * 4, 2 * hidden, db_in, 0, nullptr, st)))
-      return rc;
-  }
   const GemmPlan g = plan_gemm(kDx, rows, C, 2 * hidden, dx_add != nullptr, sms);
   rc = launch_gemm<kDx, kActNone>(K_LINEAR_DX, g, ws + L.d, w_in, nullptr, dx_add, nullptr, dx,
                                   rows, C, 2 * hidden, st);
   if (rc) return rc;
-  if ((rc = launch_dw(L.in, ws + L.d, x, rows, 2 * hidden, C, dw_in, dw_dtype, nullptr,
-                      ws + L.part_dw, nullptr, st)))
+  if ((rc = launch_dw(L.in, ws + L.d, x, rows, 2 * hidden, C, dw_in, dw_dtype, db_in,
+                      ws + L.part_dw, p.part, L.f.splits * 4, st)))
     return rc;
   return launch_dw(L.out, dy, ws + L.h, rows, C, hidden, dw_out, dw_dtype, db_out, ws + L.part_dw,
-                   ws + L.part_db, st);
+                   ws + L.part_db, 0, st);
 }
 
 }  // extern "C"
