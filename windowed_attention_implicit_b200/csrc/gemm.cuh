@@ -770,7 +770,7 @@ struct DwParams {
   int a_chunks, b_chunks;          // 64-channel chunks of a tile: dz (2 .. 4), x (1 .. 3)
   int m_tiles, n_tiles, splits, stages;
   int steps, steps_per_split;      // 64-row steps, in all and per split
-  float* part;                     // [splits][N][K]; with one split dW itself, if fp32
+  int part;                        // tm_part is written: the partials, or with one split an fp32 dW
   __nv_bfloat16* out16;            // one split and a bf16 dW
   float* part_db;                  // [splits][N]; null: no db
   uint64_t wait_limit_ns;
@@ -790,11 +790,11 @@ __host__ __device__ __forceinline__ size_t dw_smem_bytes(int a_chunks, int b_chu
 }
 
 // grid m_tiles * n_tiles * splits, block kDwThreads, dynamic smem dw_smem_bytes().
-// tm_z: dz [rows][N], tm_x: x [rows][K], boxes of 64 channels x 64 rows,
-// 128-byte swizzle.
+// tm_z: dz [rows][N], tm_x: x [rows][K], boxes of 64 channels x 64 rows; tm_part:
+// part [splits][N][K], boxes 32 x 32 x 1; 128-byte swizzle.
 __global__ void __launch_bounds__(kDwThreads, 1)
     dw_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_x,
-              const DwParams p) {
+              const __grid_constant__ CUtensorMap tm_part, const DwParams p) {
   extern __shared__ uint8_t dwg_raw[];
   uint8_t* base = dwg_raw + ((1024u - (smem_u32(dwg_raw) & 1023u)) & 1023u);
   const uint32_t stage_bytes = dw_stage_bytes(p.a_chunks, p.b_chunks);
@@ -880,24 +880,46 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // second block, whose other rows are the next tile's)
       const int n_end = min(p.N, m0 + 64 * p.a_chunks);
       const size_t row = static_cast<size_t>(split) * p.N + n;
-      const size_t part_n = static_cast<size_t>(p.splits) * p.N * p.K;
+      if (ok && p.part && n - lane < n_end) {
+        // fp32: 32 columns at a time through shared memory, whose stages are
+        // all consumed, and a bulk store: a row per lane, stored directly, would
+        // be half sectors all over the rows
+        uint8_t* sg = base + warp * 8192;
+#pragma unroll
+        for (int c = 0; c < kDwBn / 32; ++c) {
+          if (c >= 2 * b_chunks || k0 + 32 * c >= p.K) continue;
+          uint8_t* dst = sg + (c & 1) * 4096 + lane * 128;   // 128-byte swizzle
+          if (lane == 0 && c >= 2) bulk_store_wait_read_one();
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(dst + ((e ^ (lane & 7)) << 4)) =
+                make_float4(sum[32 * c + 4 * e], sum[32 * c + 4 * e + 1], sum[32 * c + 4 * e + 2],
+                            sum[32 * c + 4 * e + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_part, sg + (c & 1) * 4096, k0 + 32 * c, n, split);
+            tma_store_commit();
+          }
+        }
+      }
       if (ok && n < n_end) {
+        const size_t all = static_cast<size_t>(p.N) * p.K;
 #pragma unroll
         for (int c = 0; c < kDwBn / 4; ++c) {
           const int k = k0 + 4 * c;
-          const size_t at = row * p.K + k;
-          if (c >= 16 * b_chunks || k >= p.K || !rib_guard(at + 3, part_n, G_DW_PART)) continue;
-          if (p.out16)
-            *reinterpret_cast<uint2*>(p.out16 + at) =
-                make_uint2(pack_bf16x2(sum[4 * c], sum[4 * c + 1]),
-                           pack_bf16x2(sum[4 * c + 2], sum[4 * c + 3]));
-          else
-            *reinterpret_cast<float4*>(p.part + at) =
-                make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]);
+          const size_t at = row * p.K + k;   // one split
+          if (!p.out16 || c >= 16 * b_chunks || k >= p.K || !rib_guard(at + 3, all, G_DW_PART))
+            continue;
+          *reinterpret_cast<uint2*>(p.out16 + at) =
+              make_uint2(pack_bf16x2(sum[4 * c], sum[4 * c + 1]),
+                         pack_bf16x2(sum[4 * c + 2], sum[4 * c + 3]));
         }
         if (with_db && rib_guard(row, static_cast<size_t>(p.splits) * p.N, G_DW_PART))
           p.part_db[row] = sum_db;
       }
+      if (lane == 0) tma_store_wait_all();
     }
   } else {
     regs_dec<kDwOtherRegs>();

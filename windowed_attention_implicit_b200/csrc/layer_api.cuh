@@ -303,7 +303,17 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   p.a_chunks = d.a_chunks; p.b_chunks = d.b_chunks;
   p.m_tiles = d.m_tiles; p.n_tiles = d.n_tiles; p.splits = d.splits; p.stages = d.stages;
   p.steps = d.steps; p.steps_per_split = d.per_split;
-  p.part = static_cast<float*>(direct ? (f32 ? dw : nullptr) : part);
+  float* out = static_cast<float*>(direct ? (f32 ? dw : nullptr) : part);
+  CUtensorMap tp = tz;   // not looked at without `out`
+  if (out) {
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)d.splits};
+    const uint64_t strides[2] = {4ull * K, 4ull * N * K};
+    const uint32_t box[3] = {32, 32, 1};
+    if ((rc = make_map(&tp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B)))
+      return rc;
+  }
+  p.part = out != nullptr;
   p.out16 = direct && !f32 ? static_cast<__nv_bfloat16*>(dw) : nullptr;
   p.part_db = !db || db_rows ? nullptr : direct ? db : static_cast<float*>(part_db);
   p.wait_limit_ns = g_wait_limit_ns;
@@ -311,12 +321,13 @@ int launch_dw(const DwPlan& d, const void* dz, const void* x, int rows, int N, i
   if ((rc = set_smem(dw_kernel, smem))) return rc;
   {
     TraceScope ts(K_DW, st);
-    rc = launch(dw_kernel, dim3(d.m_tiles * d.n_tiles * d.splits), kDwThreads, smem, st, 1, tz, tx, p);
+    rc = launch(dw_kernel, dim3(d.m_tiles * d.n_tiles * d.splits), kDwThreads, smem, st, 1, tz, tx, tp,
+                p);
     if (rc) return rc;
   }
   const size_t n4 = direct ? 0 : (size_t)N * K / 4, nb4 = db && (db_rows || !direct) ? N / 4 : 0;
   if (n4 + nb4 == 0) return rc;
-  return launch_dw_reduce(p.part, d.splits, n4, static_cast<const float*>(part_db),
+  return launch_dw_reduce(out, d.splits, n4, static_cast<const float*>(part_db),
                           db_rows ? db_rows : d.splits, nb4, f32 ? static_cast<float*>(dw) : nullptr,
                           f32 ? nullptr : static_cast<__nv_bfloat16*>(dw), db, st);
 }
