@@ -11,7 +11,17 @@
 //   sum over rows of dg and du                  (fp32, before the rounding)
 // One tile is 128 rows x 64 hidden channels with three accumulators (g | u as
 // one MMA of 128 columns, then dh), two sets of them in tensor memory; the
-// warp roles are gemm.cuh's.
+// warp roles are gemm.cuh's with eight epilogue warps.
+//
+// 147456 rows, 192 channels, 384 hidden: 101 us for 453 MB, 4.5 TB/s; the whole
+// backward moves 1290 MB in 262 us, 4.9 TB/s where a plain read gets 5.2.
+// Nor epilogue (without its arithmetic 117 us for 119, before the following) nor
+// stores (102 without any) bound it but the latency of x and dy, read once per
+// column tile, mostly from L2: so the staging takes 16 columns at a time and a
+// fourth stage of x and dy fits beside the resident weights (119 -> 107 us; the
+// next kernel then meets more writes still on their way: 265 -> 262 in all).
+// Not kept: sixteen epilogue warps (124), tiles of 256 x 128 by CTA pairs, which
+// halve those reads but hold their accumulators longer (132).
 #pragma once
 
 #include "gemm.cuh"
@@ -22,7 +32,7 @@ constexpr int kFfnThreads = 320;
 constexpr int kFfnCols = 64;                              // hidden channels of a tile
 constexpr uint32_t kFfnA = 2u * kGemmATile;               // x and dy, 64 channels deep
 constexpr uint32_t kFfnB = 3u * 8192u;                    // Wg, Wu (K-major), Wo (MN-major)
-constexpr uint32_t kFfnOut = 32u * 64u;                   // a warp's staging: 32 rows x 32 columns
+constexpr uint32_t kFfnOut = 32u * 32u;                   // a warp's staging: 32 rows x 16 columns
 constexpr uint32_t kFfnStaging = 8u * 3u * kFfnOut;
 constexpr int kFfnMaxStages = 6;
 
@@ -75,8 +85,8 @@ __device__ __forceinline__ void ffn_load_b(uint8_t* dst, const CUtensorMap* tm_i
 
 // Work items and grid as in gemm_kernel.  tm_x, tm_dy: [M][C], boxes 64 x
 // 128; tm_in: w_in [2 H][C], boxes 64 x 64; tm_out: w_out [C][H], boxes 64 x
-// 64 (all 128-byte swizzle); tm_h: h [M][H], boxes 32 x 32, tm_d: dg | du
-// [M][2][H], boxes 32 x 1 x 32 (64-byte swizzle).
+// 64 (all 128-byte swizzle); tm_h: h [M][H], boxes 16 x 32, tm_d: dg | du
+// [M][2][H], boxes 16 x 1 x 32 (32-byte swizzle).
 template <int ACT>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -221,8 +231,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         if (!(ok = warp_wait(&bb.acc_full[a], (t >> 1) & 1, ab, lim, SITE_FFN))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256 * a + lane_off + 32 * half;
-        if (lane == 0) tma_store_wait_read_all();   // the last tile's stores have read the staging
-        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t g[16], u[16], d[16];
@@ -268,10 +276,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             uw[2 * e] = pack_bf16x2(du[4 * e], du[4 * e + 1]);
             uw[2 * e + 1] = pack_bf16x2(du[4 * e + 2], du[4 * e + 3]);
           }
-          // rows of 64 bytes, 64-byte swizzle: granule XOR (row / 2) % 4
+          if (lane == 0) tma_store_wait_read_all();   // the last stores have read the staging
+          __syncwarp();
+          // rows of 32 bytes, 32-byte swizzle: granule XOR (row / 4) % 2
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            uint8_t* dst = sg + lane * 64 + (((2 * h + e) ^ ((lane >> 1) & 3)) << 4);
+            uint8_t* dst = sg + lane * 32 + ((e ^ ((lane >> 2) & 1)) << 4);
             *reinterpret_cast<uint4*>(dst) =
                 make_uint4(hw[4 * e], hw[4 * e + 1], hw[4 * e + 2], hw[4 * e + 3]);
             *reinterpret_cast<uint4*>(dst + kFfnOut) =
@@ -279,20 +289,20 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             *reinterpret_cast<uint4*>(dst + 2 * kFfnOut) =
                 make_uint4(uw[4 * e], uw[4 * e + 1], uw[4 * e + 2], uw[4 * e + 3]);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < p.M && n0 + 16 * h < p.H) {
+            tma_store_2d(&tm_h, sg, n0 + 16 * h, row0);
+            tma_store_3d(&tm_d, sg + kFfnOut, n0 + 16 * h, 0, row0);
+            tma_store_3d(&tm_d, sg + 2 * kFfnOut, n0 + 16 * h, 1, row0);
+            tma_store_commit();
+          }
           if (p.part) {
             // rows beyond M: x and dy are the TMA's zeros, so dh = 0 and they
             // add nothing
             sum_g[h] += col_sum16(dg, lane);
             sum_u[h] += col_sum16(du, lane);
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && row0 < p.M && n0 < p.H) {
-          tma_store_2d(&tm_h, sg, n0, row0);
-          tma_store_3d(&tm_d, sg + kFfnOut, n0, 0, row0);
-          tma_store_3d(&tm_d, sg + 2 * kFfnOut, n0, 1, row0);
-          tma_store_commit();
         }
       }
       if (ok && p.part && (lane & 1) == 0) {

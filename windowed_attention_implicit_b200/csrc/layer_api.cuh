@@ -579,13 +579,13 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
   if (!rc) rc = map_2d(&ty, dy, p.M, p.C, 64, 128);
   if (!rc) rc = map_2d(&ti, w_in, 2ull * p.H, p.C, 64, 64);
   if (!rc) rc = map_2d(&to, w_out, p.C, p.H, 64, 64);
-  if (!rc) rc = map_2d(&th, ws + w.h, p.M, p.H, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!rc) rc = map_2d(&th, ws + w.h, p.M, p.H, 16, 32, CU_TENSOR_MAP_SWIZZLE_32B);
   if (!rc) {
     const uint64_t dims[3] = {(uint64_t)p.H, 2, (uint64_t)p.M};
     const uint64_t strides[2] = {2ull * p.H, 4ull * p.H};
-    const uint32_t box[3] = {32, 1, 32};
+    const uint32_t box[3] = {16, 1, 32};
     rc = make_map(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ws + w.d, dims, strides, box,
-                  CU_TENSOR_MAP_SWIZZLE_64B);
+                  CU_TENSOR_MAP_SWIZZLE_32B);
   }
   if (rc) return rc;
   if ((rc = set_smem(ffn_bwd_kernel<ACT>, w.f.smem))) return rc;
