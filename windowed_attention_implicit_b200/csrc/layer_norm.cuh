@@ -13,12 +13,16 @@
 // ln_async_kernel (up to 1024 channels): every warp runs its own pipeline over
 // blocks of a few rows.  Rows are contiguous, so a block is one run of bytes
 // whatever the channel count, odd ones included: a bulk copy brings it into
-// one of two or three shared-memory stages, the warp works on it there, writes y (or
-// dx) over x (or dy) and a bulk copy takes it back.  The next blocks are in
-// flight meanwhile, without holding registers, and no warp waits for another.  L lanes hold a row as vectors of V elements,
-// vector j + L i in lane j, so 192 channels of bf16 use all 32 lanes (four
-// rows of eight lanes, three vectors each) where a lane per vector would
-// idle a quarter of them.
+// one of two or three shared-memory stages, the warp works on it there, writes
+// y (or dx) over x (or dy) and a bulk copy takes it back.  The next blocks are
+// in flight meanwhile, without holding registers, and no warp waits for
+// another.  L lanes hold a row as vectors of V elements, vector j + L i in lane
+// j, so 192 channels of bf16 use all 32 lanes (four rows of eight lanes, three
+// vectors each) where a lane per vector would idle a quarter of them.
+// Measured, bf16, 192 channels: forward of 294912 rows 40 us (226 MB, 5.7 TB/s),
+// backward of 147456 with a second gradient 41.5 us (226 MB and the sums); fp32,
+// 333 channels, backward of 9217 rows 23 us: 49 MB, but single elements in
+// shared memory and four rounds of blocks bound it, not HBM.
 //
 // ln_row_*_kernel (wider rows, or pointers off a 16-byte address): a group of
 // threads (a CTA above 1024 channels, else a warp) holds a row in registers.
