@@ -432,7 +432,8 @@ int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C
  *   act      : RIB_ACT_*
  *   residual : bf16 [rows][N] or NULL
  *   pre      : out, bf16 [rows][N], z for the backward, or NULL
- *   y        : out, bf16 [rows][N]; may be residual
+ *   y        : out, bf16 [rows][N]; may be residual, not x (RIB_ERR_ARG);
+ *              pre is neither of these
  * z, act(z) and the sum are fp32; y and pre are each rounded once.
  * ------------------------------------------------------------------------ */
 int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const float* bias,
@@ -446,12 +447,13 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
  *              RIB_ACT_NONE
  *   dy       : bf16 [rows][N]
  *   dx_add   : bf16 [rows][K] or NULL, a second gradient of x
- *   dx       : out, bf16 [rows][K], or NULL; may be dx_add
+ *   dx       : out, bf16 [rows][K], or NULL; may be dx_add, not x or dy
+ *              (RIB_ERR_ARG)
  *   dw       : out, [N][K] of dw_dtype (RIB_DTYPE_*), or NULL
  *   db       : out, fp32 [N], or NULL
  *   workspace: device, >= rib_linear_bwd_workspace() bytes, 256-byte aligned
  * Through an activation dz is rounded to bf16 for the two products (dW then
- * carries that rounding, relative 2^-9 per term, whatever its type); db is
+ * carries that rounding, relative 2^-8 per term, whatever its type); db is
  * summed from the fp32 dz.
  * ------------------------------------------------------------------------ */
 size_t rib_linear_bwd_workspace(int rows, int K, int N, int act);
@@ -487,7 +489,7 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
  *   dx = dg Wg + du Wu + dx_add,  dWg = dg^T x,  dWu = du^T x,  dWo = dy^T h,
  *   dbg, dbu, dbo = sum_rows dg, du, dy.
  *
- *   dx     : out, bf16 [rows][C]; may be dx_add
+ *   dx     : out, bf16 [rows][C]; may be dx_add, not x or dy (RIB_ERR_ARG)
  *   dw_in  : out, [2][hidden][C];  dw_out : out, [C][hidden], of dw_dtype
  *   db_in  : out, fp32 [2][hidden] or NULL;  db_out : out, fp32 [C] or NULL
  *   workspace : device, >= rib_gated_ffn_bwd_workspace() bytes, 256-byte

@@ -83,6 +83,21 @@ def test_refusals(fn, kw, code):
     assert fn(**kw) == code
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="stand-in pointers: only where nothing can be launched")
+@pytest.mark.parametrize("fn,outs,clash", [
+    (lin_fwd, ("residual", "pre", "y"), [("y", "x"), ("pre", "x"), ("pre", "y"), ("pre", "residual")]),
+    (lin_bwd, ("dy", "dx_add", "dx"), [("dx", "x"), ("dx", "dy")]),
+    (ffn_bwd, ("dy", "dx_add", "dx"), [("dx", "x"), ("dx", "dy")])])
+def test_outputs_over_inputs_that_are_read_later_are_refused(fn, outs, clash):
+    apart = {n: FAKE + ((i + 1) << 24) for i, n in enumerate(outs)}
+    assert fn(**apart) not in (_abi.RIB_OK, ARG, ALIGN, UNS)    # only the missing device is left to refuse
+    for out, other in clash:
+        assert fn(**{**apart, out: apart.get(other, FAKE)}) == ARG
+    last = {"y": "residual"} if "y" in outs else {"dx": "dx_add"}
+    for out, other in last.items():                              # in place of these it may be
+        assert fn(**{**apart, out: apart[other]}) not in (_abi.RIB_OK, ARG, ALIGN, UNS)
+
+
 def test_no_rows_is_valid_and_reads_no_pointer():
     assert ln_fwd(rows=0, x=None, y=None) == _abi.RIB_OK
     assert lin_fwd(rows=0, x=None, w=None, y=None) == _abi.RIB_OK

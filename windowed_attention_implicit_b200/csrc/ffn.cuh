@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  settle(ab);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

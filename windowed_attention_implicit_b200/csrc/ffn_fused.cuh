@@ -153,9 +153,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
       }
-      if (*ab)   // far longer than the loads in flight take; the CTAs leave together
-        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
-        }
     }
   } else if (warp == kGemmMmaWarp) {
     // ---------------------------------------------------------- MMA issue
@@ -386,6 +383,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  settle(ab);
   cluster_sync();
   if (warp == kGemmMmaWarp) {
     tc_fence_after();

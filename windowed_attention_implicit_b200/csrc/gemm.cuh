@@ -72,6 +72,15 @@ __device__ __forceinline__ int warp_index() {
   return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
 }
 
+// Behind the last barrier of a CTA whose waits ran out: a load issued by a
+// producer that had already left could still be on its way into the CTA's
+// shared memory, so it stays for far longer than a load takes.
+__device__ __forceinline__ void settle(volatile int* aborted) {
+  if (!*aborted) return;
+  for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
+  }
+}
+
 // ---------------------------------------------------------------- CTA pairs
 // Two CTAs of a cluster work as one 256-row tile (cta_group::2): each holds
 // its 128 rows of A and of the accumulator and half of B; CTA 0 issues the
@@ -742,6 +751,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  settle(ab);
   // neither CTA of a pair leaves while the other may still read its shared
   // memory or arrive on its barriers
   if (CG == 2) cluster_sync();
@@ -998,6 +1008,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  settle(ab);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

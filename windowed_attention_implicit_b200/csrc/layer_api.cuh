@@ -725,6 +725,8 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (rows == 0) return RIB_OK;
   if (!x || !w || !y) return RIB_ERR_ARG;
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
+  // other tiles still read x, and the residual after pre is written
+  if (y == x || pre == x || pre == y || (pre && pre == residual)) return RIB_ERR_ARG;
   if (few_rows_win(rows, K, N))
     return launch_few<false>(act, x, w, bias, residual, pre, y, rows, N, K,
                              static_cast<cudaStream_t>(stream));
@@ -754,6 +756,7 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     return zero_async(db, (size_t)N * 4, st);
   }
   if (!dy || (dx && !w) || (dw && !x) || (act != RIB_ACT_NONE && !pre)) return RIB_ERR_ARG;
+  if (dx && (dx == dy || dx == x)) return RIB_ERR_ARG;   // both are read after dx is written
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   const LinearBwdWs L = linear_bwd_ws(rows, K, N, act, sms);
@@ -865,6 +868,7 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
     return zero_async(db_out, (size_t)C * 4, st);
   }
   if (!x || !w_in || !w_out || !dy || !dx) return RIB_ERR_ARG;
+  if (dx == x || dx == dy) return RIB_ERR_ARG;   // both are read after dx is written
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   const FfnBwdWs L = ffn_bwd_ws(rows, C, hidden, sms);
