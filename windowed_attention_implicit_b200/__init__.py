@@ -617,7 +617,9 @@ class _Call:
         if self.index < 0:
             raise ValueError("x must be a CUDA tensor")
         if given is None:
-            given = self.empty((max(need, 256),), torch.uint8)
+            if need == 0:   # the library does not look at it
+                return None, 0, None
+            given = self.empty((need,), torch.uint8)
         return (self.ptr("workspace", given, given.numel()), given.numel() * given.element_size(),
                 given)
 

@@ -61,19 +61,23 @@ int div_up(long long a, long long b) { return static_cast<int>((a + b - 1) / b);
 
 // How many items the row tiles of one column tile are dealt to: the count
 // with the fewest tiles on the busiest CTA, the smallest such (fewer items
-// reload fewer weights).
+// reload fewer weights), at most 2 sms.  Only the most items that finish in
+// 1, 2, ... rounds can be best, and of those the fewest with as few row tiles
+// each: a search over every count took 9 of 18 us of a call on the host.
 int pick_splits(int m_tiles, int n_tiles, int sms) {
+  const int most = std::min(m_tiles, 2 * sms);
   int best = 1;
   long long best_cost = -1;
-  for (int s = 1; s <= m_tiles && s <= 2 * sms; ++s) {
-    const long long cost =
-        (long long)div_up((long long)n_tiles * s, sms) * div_up(m_tiles, s);
+  for (int rounds = div_up(n_tiles, sms);; ++rounds) {
+    const int s = static_cast<int>(std::min<long long>(most, (long long)rounds * sms / n_tiles));
+    const int per = div_up(m_tiles, s);
+    const long long cost = (long long)div_up((long long)n_tiles * s, sms) * per;
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = s;
+      best = div_up(m_tiles, per);
     }
+    if (s == most) return best;
   }
-  return best;
 }
 
 struct GemmPlan {
@@ -256,14 +260,15 @@ DwPlan plan_dw(int rows, int N, int K, int sms) {
   d.steps = div_up(rows, 64);
   d.b_chunks = std::min(kDwBn / 64, div_up(K, 64));
   d.n_tiles = div_up(K, 64 * d.b_chunks);
+  const unsigned most = d.steps;
   double best = -1.0;
   for (int ac = 2; ac <= 4; ++ac) {
     const int m_tiles = div_up(N, 64 * ac);
     const long long tiles = (long long)m_tiles * d.n_tiles;
     const double step = std::max(0.15 * (ac + d.b_chunks), 0.32 * (ac > 2 ? 2 : 1));
-    for (int s = 1; s <= d.steps && (s == 1 || tiles * s <= 2ll * sms); ++s) {
-      const int per = div_up(d.steps, s);
-      const double cost = div_up(tiles * s, sms) * (per + 4) * step +
+    for (unsigned s = 1; s <= most && (s == 1 || tiles * s <= 2ll * sms); ++s) {
+      const unsigned per = (most + s - 1) / s;   // 32 bits: the divisions are the loop's time
+      const double cost = (static_cast<unsigned>(tiles * s) + sms - 1) / sms * (per + 4) * step +
                           (s > 1 ? 2.0 + (double)s * N * K * 8.0 / 4.0e6 : 0.0);
       if (best < 0 || cost < best) {
         best = cost;
