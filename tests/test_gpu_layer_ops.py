@@ -82,7 +82,10 @@ def _slope_err(z, act):
 
 LN_SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (33, 96), (1000, 192), (7, 250), (9, 256), (65, 264),
              (17, 512), (10, 1000), (4, 1024), (3, 1032), (6, 1025), (5, 2048), (3, 2056), (2, 4096),
-             (3, 4104), (2, 8192), (2, 8191), (20001, 8), (4099, 33)]
+             (3, 4104), (2, 8192), (2, 8191), (20001, 8), (4099, 33),
+             # single elements, a row to 8, 16 or 32 lanes
+             (9, 3), (70, 10), (20003, 10), (37, 20), (41, 36), (65, 50), (12345, 63), (33, 68), (19, 100), (77, 125),
+             (50, 130), (21, 390), (22, 601), (23, 767), (24, 770), (25, 903)]
 
 
 def _ln_case(rows, C, dtype, seed=3):

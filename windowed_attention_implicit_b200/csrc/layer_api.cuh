@@ -366,19 +366,31 @@ LnPlan plan_ln(int rows, int C, int es, bool bwd, bool aligned, int sms) {
   const int arrays = bwd ? 3 : 1;   // also without dres: the sums then run in the same order
   const int v = 16 / es;
   n.vec = aligned && C % v == 0 ? v : 1;
-  if (aligned && C <= 1024) {
+  // (the backward of more than 768 single elements spills there: 60000 x 1001 of
+  // bf16 260 us, 213 by row kernels; at 601 116)
+  if (aligned && C <= 1024 && !(bwd && n.vec == 1 && C > 768)) {
     const int vecs = C / n.vec;
-    // as few lanes per row as keep four vectors a lane; single elements are
-    // dealt to the whole warp
-    n.lanes = n.vec == 1 ? 32 : vecs <= 16 ? 4 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
-    n.nv = div_up(vecs, n.lanes * (n.vec == 1 ? 2 : 1));
-    if (n.vec == 1 || n.nv > 4) n.nv = n.nv <= 4 ? 4 : n.nv <= 8 ? 8 : 16;
+    // as few lanes per row as keep four vectors (or pairs of single elements) a
+    // lane (backward of 122931 x 10 15 us, with all 32 lanes 72; x 100 57 for 77)
+    if (n.vec == 1) {
+      n.lanes = vecs <= 64 ? 8 : vecs <= 128 ? 16 : 32;
+      n.nv = div_up(vecs, 2 * n.lanes);
+      n.nv = n.nv <= 2 && n.lanes == 8 ? 2
+             : n.nv <= 4                ? 4
+             : n.nv <= 8                ? (n.nv + 1) / 2 * 2
+                                        : (n.nv + 3) / 4 * 4;
+    } else {
+      n.lanes = vecs <= 16 ? 4 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
+      n.nv = div_up(vecs, n.lanes);
+      if (n.nv > 4) n.nv = n.nv <= 8 ? 8 : 16;
+    }
     // A block: whole groups of rows, 32 rows at most (a lane holds a row's
     // statistics).  Measured at 192 channels of bf16: the forward
     // is best at four rows (1.5 KB; 40.0 us for 294912 rows, 44 at sixteen), the
     // backward at eight (3 KB of each array; 42 us with the sums for 147456
     // rows, 56 at four: its fixed work per block is larger).
-    const int unit = n.vec == 1 ? 2 : 32 / n.lanes;   // single elements: two rows interleaved
+    // single elements: two groups of rows interleaved
+    const int unit = 32 / n.lanes * (n.vec == 1 ? 2 : 1);
     n.q.rows = std::min(std::max(1, (bwd ? 9216 : 2048) / (arrays * unit * C * es)) * unit, 32);
     n.q.bytes = (n.q.rows * C * es + (n.vec == 1 ? 32 : 0) + 127) & ~127;
     const size_t weights = ((bwd ? 1 : 2) * 4 * C + 127) & ~127;
@@ -422,7 +434,10 @@ int ln_launch_row(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st)
 
 template <typename T, int V, int NV, int L>
 int ln_launch_async(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
-  auto kernel = bwd ? ln_async_kernel<T, V, NV, L, true> : ln_async_kernel<T, V, NV, L, false>;
+  auto kernel = ln_async_kernel<T, V, NV, L, false>;
+  if constexpr (V != 1 || NV < 16) {   // plan_ln
+    if (bwd) kernel = ln_async_kernel<T, V, NV, L, true>;
+  }
   int rc = set_smem(kernel, n.smem);
   if (rc) return rc;
   LnBlocks q = n.q;
@@ -450,8 +465,13 @@ int ln_dispatch(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
   if constexpr (V == 4) {
     RIB_LN(V, 8, 32);
   }
+  RIB_LN(1, 2, 8);
+  RIB_LN(1, 4, 8);
+  RIB_LN(1, 4, 16);
   RIB_LN(1, 4, 32);
+  RIB_LN(1, 6, 32);
   RIB_LN(1, 8, 32);
+  RIB_LN(1, 12, 32);
   RIB_LN(1, 16, 32);
 #undef RIB_LN
   const int C = p.C;

@@ -21,11 +21,12 @@
 // vectors each) where a lane per vector would idle a quarter of them.
 // Measured, bf16, 192 channels: forward of 294912 rows 40 us (226 MB, 5.7 TB/s),
 // backward of 147456 with a second gradient 41.5 us (226 MB and the sums); fp32,
-// 333 channels, backward of 9217 rows 23 us: 49 MB, but single elements in
-// shared memory and four rounds of blocks bound it, not HBM.
+// 333 channels, backward of 9217 rows 22 us: 49 MB, but single elements in
+// shared memory bound it, not HBM.
 //
-// ln_row_*_kernel (wider rows, or pointers off a 16-byte address): a group of
-// threads (a CTA above 1024 channels, else a warp) holds a row in registers.
+// ln_row_*_kernel (wider rows, the backward of more than 768 channels that are
+// not whole vectors, or pointers off a 16-byte address): a group of threads (a
+// CTA above 1024 channels, else a warp) holds a row in registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -453,8 +454,8 @@ struct LnBlocks {
 
 // Slot i of a lane: what it holds of a row at a time, as P packed fp32 pairs,
 // to and from shared memory.  Whole vectors: vector j + L i (V elements, V / 2
-// pairs).  Single elements (V = 1, L = 32): elements j + 64 i and j + 64 i + 32
-// as one pair.  `row` is the row's first byte; elements beyond C read as zero
+// pairs).  Single elements (V = 1): elements j + 2 L i and j + 2 L i + L as one
+// pair.  `row` is the row's first byte; elements beyond C read as zero
 // and are not written (a vector beyond C is not asked for).
 template <typename T, int V, int L>
 struct LnSlot;
@@ -487,25 +488,25 @@ struct LnSlot<float, 4, L> {
         make_float4(lo2(f[0]), hi2(f[0]), lo2(f[1]), hi2(f[1]));
   }
 };
-template <typename T>
-struct LnSlot<T, 1, 32> {
+template <typename T, int L>
+struct LnSlot<T, 1, L> {
   static constexpr int P = 1;
   static __device__ __forceinline__ void get(const uint8_t* row, int i, int j, int C, uint64_t (&f)[1]) {
     const T* r = reinterpret_cast<const T*>(row);
-    const int c = j + 64 * i;
-    f[0] = pk2(c < C ? static_cast<float>(r[c]) : 0.f, c + 32 < C ? static_cast<float>(r[c + 32]) : 0.f);
+    const int c = j + 2 * L * i;
+    f[0] = pk2(c < C ? static_cast<float>(r[c]) : 0.f, c + L < C ? static_cast<float>(r[c + L]) : 0.f);
   }
   static __device__ __forceinline__ void put(uint8_t* row, int i, int j, int C, const uint64_t (&f)[1]) {
     T* r = reinterpret_cast<T*>(row);
-    const int c = j + 64 * i;
+    const int c = j + 2 * L * i;
     if (c < C) r[c] = static_cast<T>(lo2(f[0]));   // to nearest
-    if (c + 32 < C) r[c + 32] = static_cast<T>(hi2(f[0]));
+    if (c + L < C) r[c + L] = static_cast<T>(hi2(f[0]));
   }
 };
 // column of half h of pair e of slot i
 template <int V, int L>
 __device__ __forceinline__ int ln_column(int i, int j, int e, int h) {
-  return V == 1 ? j + 64 * i + 32 * h : (j + L * i) * V + 2 * e + h;
+  return V == 1 ? j + 2 * L * i + L * h : (j + L * i) * V + 2 * e + h;
 }
 
 template <int L>
@@ -527,8 +528,8 @@ __device__ __forceinline__ int ln_weight_slot(int c, int C) {
 template <int V, int L, int P>
 __device__ __forceinline__ void ln_weight_get(const float* w, int i, int j, int C, uint64_t (&f)[P]) {
   if constexpr (V == 1) {
-    const int c = j + 64 * i;
-    f[0] = pk2(c < C ? w[c] : 0.f, c + 32 < C ? w[c + 32] : 0.f);
+    const int c = j + 2 * L * i;
+    f[0] = pk2(c < C ? w[c] : 0.f, c + L < C ? w[c + L] : 0.f);
   } else {
 #pragma unroll
     for (int h = 0; h < V / 4; ++h) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
   constexpr int P = LP::P;
   constexpr int G = 32 / L;   // rows side by side
   // rows whose chains of shuffles run interleaved, where the registers allow
-  constexpr int RR = L == 32 && NV * P <= 8 ? 2 : 1;
+  constexpr int RR = (L == 32 || V == 1) && NV * P <= 8 ? 2 : 1;
   constexpr uint32_t ES = sizeof(T);
   extern __shared__ __align__(128) uint8_t ln_smem[];
   __shared__ int abort_flag;
