@@ -473,7 +473,8 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
  *   y      : out, bf16 [rows][C]; may be residual
  *   workspace : device, >= rib_gated_ffn_fwd_workspace() bytes (h, where two
  *            products are faster than one kernel; 0: may be NULL) on the current
- *            device, 256-byte aligned
+ *            device, 256-byte aligned; to be asked for each number of rows, fewer
+ *            rows can need more
  * h is rounded to bf16, as the second product takes it; y once.  hidden <= 32768.
  * ------------------------------------------------------------------------ */
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden);
