@@ -5,21 +5,29 @@
 // A pair of CTAs (cta_group::2, gemm.cuh) owns 256 rows.  Their x stays in
 // shared memory and their y (256 x C) in tensor memory while the pair walks
 // the hidden channels 64 at a time: an MMA of 128 columns gives the chunk's
-// gate and other projection, the epilogue warps turn it into 64 columns of h
-// in shared memory, and a second MMA adds h Wo^T to y.  h never reaches HBM:
-// at 192 channels and 384 hidden ones that is 226 of 396 MB.  What is read
-// again per row tile are the weights, from L2; each CTA of a pair reads half.
+// gate and other projection (GU), the epilogue warps turn it into 64 columns of
+// h, and a second MMA adds h Wo^T to y (Y).  h never reaches HBM: at 192 channels
+// and 384 hidden ones that is 226 of 396 MB.  What is read again per row tile are
+// the weights, from L2; each CTA of a pair reads half.
+//
+// h lies in tensor memory, where Y takes its A operand from: each warp writes
+// its 16 channels of h (bf16 pairs, 8 columns, one step of the MMA) over the
+// 16 gate columns that it has just read, in its own CTA's lanes.  That makes
+// the hand-over to CTA 0, which issues the MMAs for both, one of tensor memory
+// only, ordered by the tcgen05 fences around the arrival and the wait.  (Through
+// shared memory, CTA 1's h would have to be published to CTA 0 at cluster
+// scope, which took 107 us of 147456 x 192 x 384 rows for 86, by a relay in each
+// CTA as by releases from every warp.)
 //
 // Order of the work, with chunk g of all the pair's chunks:
-//   MMA        GU(0), GU(1), GU(2), Y(0), GU(3), Y(1), ...   so that two GU are
-//              queued while the epilogue of a chunk runs (with one ahead 147456 x
-//              192 x 768 took 158 us for 154; where the ring holds two chunks'
-//              weights only, above 192 channels, one)
+//   MMA        GU(0), GU(1), Y(0), GU(2), Y(1), GU(3), ...   GU(g + 2) takes the
+//              columns of h(g) and so waits for Y(g); the epilogue has GU(g + 1)
+//              meanwhile, and is much the longer
 //   epilogue   h(0), h(1), ...; y of a row tile after the first h of the next
 //              one; y leaves tensor memory before it is worked on, so that the
 //              next tile's Y can start, and its residual is loaded one chunk
 //              ahead
-// Two accumulators of 128 columns for GU, one of C for y, two h tiles.
+// Two accumulators of 128 columns for GU and h, one of C for y.
 #pragma once
 
 #include "gemm.cuh"
@@ -28,7 +36,6 @@ namespace rib {
 
 constexpr int SITE_FUSED = 53;
 constexpr int kFusedMaxC = 256;
-constexpr uint32_t kFusedH = 128u * 128u;      // h: 128 rows x 64 channels of a CTA
 constexpr int kFusedMaxRing = 4;
 
 struct FusedParams {
@@ -43,7 +50,7 @@ struct FusedBars {
   uint64_t x_full, x_free, y_full, y_free;
   uint64_t in_full[kFusedMaxRing], in_free[kFusedMaxRing];
   uint64_t out_full[kFusedMaxRing], out_free[kFusedMaxRing];
-  uint64_t gu_full[2], gu_free[2], h_full[2], h_free[2];
+  uint64_t gu_full[2], h_full[2], y_done[2];
   uint64_t drain, res[kGemmEpiWarps];
   uint32_t tmem;
   int abort_flag;
@@ -55,8 +62,8 @@ __host__ __device__ __forceinline__ uint32_t fused_in_bytes(int C) { return (C +
 __host__ __device__ __forceinline__ uint32_t fused_out_bytes(int C) { return fused_cols(C) / 2 * 128u; }
 __host__ __device__ __forceinline__ size_t fused_smem_bytes(int C, int ring) {
   return 1024 + static_cast<size_t>((C + 63) / 64) * kGemmATile +
-         static_cast<size_t>(ring) * (fused_in_bytes(C) + fused_out_bytes(C)) + 2 * kFusedH +
-         kGemmStaging + sizeof(FusedBars);
+         static_cast<size_t>(ring) * (fused_in_bytes(C) + fused_out_bytes(C)) + kGemmStaging +
+         sizeof(FusedBars);
 }
 
 // tm_x: [M][C], boxes 64 x 128; tm_in: w_in [2 H][C], boxes 64 x 64; tm_out: w_out
@@ -77,8 +84,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t x_bytes = p.k_steps * kGemmATile;
   uint8_t* s_in = s_x + x_bytes;
   uint8_t* s_out = s_in + p.ring * in_bytes;
-  uint8_t* s_h = s_out + p.ring * out_bytes;
-  uint8_t* s_stage = s_h + 2 * kFusedH;
+  uint8_t* s_stage = s_out + p.ring * out_bytes;
   FusedBars& bb = *reinterpret_cast<FusedBars*>(s_stage + kGemmStaging);
   volatile int* ab = &bb.abort_flag;
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -99,9 +105,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bb.gu_full[i], 1);
-      mbar_init(&bb.gu_free[i], 2 * kGemmEpiWarps);
       mbar_init(&bb.h_full[i], 2 * kGemmEpiWarps);
-      mbar_init(&bb.h_free[i], 1);
+      mbar_init(&bb.y_done[i], 1);
     }
     mbar_init(&bb.drain, 1);
     for (int i = 0; i < kGemmEpiWarps; ++i) mbar_init(&bb.res[i], 1);
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bb.tmem;   // y at 0, GU at 256 and 384
+  const uint32_t tmem = bb.tmem;   // y at 0, GU (and h over it) at 256 and 384
 
   if (warp == kGemmTmaWarp) {
     // ---------------------------------------------------------- TMA producer
@@ -172,12 +177,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!(ok = warp_wait(&bb.out_full[st_out], ph_out, ab, lim, SITE_FUSED))) return;
         if (!(ok = warp_wait(&bb.h_full[g & 1], (g >> 1) & 1, ab, lim, SITE_FUSED))) return;
         tc_fence_after();
-        pair_umma_steps<2>(c + 1 == p.chunks ? last_h : 4, tmem,
-                           make_sdesc(smem_u32(s_h + (g & 1) * kFusedH), 16, 1024, kLayoutSW128), 2,
+        pair_umma_ts_steps(c + 1 == p.chunks ? last_h : 4, tmem, tmem + 256 + 128 * (g & 1),
                            make_sdesc(smem_u32(s_out + st_out * out_bytes), 16, 1024, kLayoutSW128),
                            2, id_y, c > 0 ? 1u : 0u);
+        pair_commit<2>(&bb.y_done[g & 1]);
         pair_commit<2>(&bb.out_free[st_out]);
-        pair_commit<2>(&bb.h_free[g & 1]);
         if (c + 1 == p.chunks) pair_commit<2>(&bb.y_full);
         if (++st_out == p.ring) {
           st_out = 0;
@@ -185,14 +189,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       };
       int c = 0, t = 0, c_y = 0, t_y = 0;   // chunk and tile of the next GU and Y
-      // two GU ahead of Y where the ring holds the weights for it
-      const int ahead = p.ring > 2 ? 2 : 1;
-      for (int g = 0; ok && g < total + ahead; ++g) {
+      for (int g = 0; ok && g <= total; ++g) {
         if (g < total) {
           if (c == 0 && !(ok = warp_wait(&bb.x_full, t & 1, ab, lim, SITE_FUSED))) break;
           if (!(ok = ring.wait(&bb.in_full[st_in], ph_in, ab, lim, SITE_FUSED))) break;
-          if (g >= 2 &&
-              !(ok = warp_wait(&bb.gu_free[g & 1], ((g >> 1) - 1) & 1, ab, lim, SITE_FUSED)))
+          // Y(g - 2) has read h from the columns (and the epilogue has left them)
+          if (g >= 2 && !(ok = warp_wait(&bb.y_done[g & 1], ((g >> 1) - 1) & 1, ab, lim, SITE_FUSED)))
             break;
           tc_fence_after();
           const uint32_t sa = smem_u32(s_x), sb = smem_u32(s_in + st_in * in_bytes);
@@ -214,8 +216,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           ring.peek(&bb.in_full[st_in], ph_in);
         }
-        if (g >= ahead) {
-          issue_y(g - ahead, c_y, t_y);
+        if (g > 0) {
+          issue_y(g - 1, c_y, t_y);
           if (++c_y == p.chunks) {
             c_y = 0;
             ++t_y;
@@ -327,8 +329,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_wait_ld();
         reg_fence_x16(v);
         reg_fence_x16(w);
-        tc_fence_before();
-        to_leader(&bb.gu_free[g & 1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           auto f = [](uint32_t x) { return __uint_as_float(x); };
@@ -342,15 +342,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           out[2 * e] = in ? pack_bf16x2(lo2(z01), hi2(z01)) : 0u;
           out[2 * e + 1] = in ? pack_bf16x2(lo2(z23), hi2(z23)) : 0u;
         }
-        if (g >= 2 && !(ok = warp_wait(&bb.h_free[g & 1], ((g >> 1) - 1) & 1, ab, lim, SITE_FUSED)))
-          break;
-        const int r = 32 * quarter + lane;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          *reinterpret_cast<uint4*>(s_h + (g & 1) * kFusedH + r * 128 +
-                                    (((2 * group + q) ^ (r & 7)) << 4)) =
-              make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
-        fence_proxy_async_smem();
+        tmem_st_x8(acc, out);
+        tmem_wait_st();
+        tc_fence_before();
         to_leader(&bb.h_full[g & 1]);
       }
       // a unit of the previous tile's y behind each of this tile's first

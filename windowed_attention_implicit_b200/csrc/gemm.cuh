@@ -99,9 +99,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// (CTA scope: what it orders are tensor-memory reads, which the tcgen05 fence
-// before it and the one after the wait order; a cluster-scope release also
-// waits for all earlier stores, about 2400 cycles.)
+// An arrival on a barrier of the other CTA that hands over tensor memory, and
+// nothing else: what it orders are tensor-memory reads and writes, which the
+// tcgen05 fence before it and the one after the wait order, so CTA scope will do.
+// It does not order shared memory for the other CTA: that takes a release and an
+// acquire at cluster scope, and the release waits for all earlier stores, about
+// 2400 cycles.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -191,6 +194,46 @@ __device__ __forceinline__ void pair_umma_steps(int steps, uint32_t d, uint64_t 
     for (int s = 0; s < steps; ++s)
       pair_umma<CG>(d, a + static_cast<uint64_t>(a_step) * s, b + static_cast<uint64_t>(b_step) * s,
                     idesc, s > 0 ? 1u : first_acc);
+  }
+}
+
+// Four MMAs D (+)= A_k B_k of a pair with A in tensor memory, each CTA's 128 rows
+// in its own lanes: 16 bf16 channels a step in 8 columns, 16 columns from one
+// step to the next; B's descriptor advances by b_step.  One election.
+__device__ __forceinline__ void pair_umma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t b_step,
+                                              uint32_t idesc, uint32_t first_acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 b, sb;\n\t.reg .b32 a;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, %4, %4;\n\t"
+      "cvt.u64.u32 sb, %3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+      "add.s32 a, %1, 16;\n\t add.s64 b, %2, sb;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "add.s32 a, a, 16;\n\t add.s64 b, b, sb;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "add.s32 a, a, 16;\n\t add.s64 b, b, sb;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(b_step), "r"(idesc), "r"(first_acc)
+      : "memory");
+}
+// `steps` (1 .. 4) of them
+__device__ __forceinline__ void pair_umma_ts_steps(int steps, uint32_t d, uint32_t a, uint64_t b,
+                                                   uint32_t b_step, uint32_t idesc,
+                                                   uint32_t first_acc) {
+  if (steps == 4) {
+    pair_umma_ts4(d, a, b, b_step, idesc, first_acc);
+  } else {
+    for (int s = 0; s < steps; ++s)
+      asm volatile(
+          "{\n\t.reg .pred p, e;\n\t"
+          "setp.ne.b32 p, %4, 0;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\t"
+          "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+          "r"(a + 16 * s), "l"(b + static_cast<uint64_t>(b_step) * s), "r"(idesc),
+          "r"(s > 0 ? 1u : first_acc)
+          : "memory");
   }
 }
 

@@ -623,12 +623,14 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
 
 // A pair takes the same time for a row tile however few tiles there are, and
 // the two products spread few rows over more SMs: one kernel wins from a tile
-// per pair on (147456 rows, silu, residual: 192 x 384 92 us for 92, 192 x 768
-// 154 for 159, 96 x 384 74 for 83; 65536 x 256 x 1024 111 for 116; without a
-// residual 81 for 82, 138 for 149, 65 for 79, 98 for 121; at worst, 149 tiles on
-// 74 pairs, 58 for 52), below that where a tile is short (4096 x 96 x 192 8.9 for
-// 9.8; 9216 x 192 x 384 15 for 16; 8192 x 128 x 512 15.9 for 16.1; but 4096 x 128 x
-// 512 15.5 for 13.5, 8192 x 256 x 1024 30 for 24.5).
+// per pair on (147456 rows, silu, residual: 192 x 384 86 us for 93, 192 x 768
+// 142 for 165, 96 x 384 63 for 91; 102400 x 256 x 1024 152 for 168), also where
+// the last round of pairs is nearly empty (75 tiles on 74 pairs, 192 x 384 22.0
+// for 25.3, 192 x 768 36.0 for 38.0, 256 x 1024 50.4 for 52.7; the one size found
+// where it loses is 149 tiles of 192 x 768, 52.4 for 50.7); below that where a
+// tile is short (4096 x 96 x 192 8.0 for 9.8; 9216 x 192 x 384 13.3 for 15.3; 8192 x
+// 128 x 512 14.0 for 15.4; but 4096 x 128 x 512 13.8 for 13.0, 2304 x 192 x 384
+// 12.9 for 11.4, 8192 x 256 x 1024 27.3 for 23.1).
 bool fused_wins(int rows, int C, int hidden, int sms) {
   const int tiles = div_up(rows, 256);
   return C <= kFusedMaxC && (tiles >= sms / 2 || tiles >= 3 * div_up(hidden, 64));
