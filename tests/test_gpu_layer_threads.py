@@ -1,4 +1,6 @@
-"""Calls from host threads other than the one that set everything up."""
+"""Calls from host threads other than the one that set everything up, one at a
+time and two at once."""
+import sys
 import threading
 
 import pytest
@@ -10,6 +12,7 @@ import windowed_attention_implicit_b200 as R
 pytestmark = pytest.mark.gpu
 
 bf, f32 = torch.bfloat16, torch.float32
+CALLS = 20000
 
 
 def _rand(shape, seed, std=1.0, dtype=bf):
@@ -82,3 +85,51 @@ def test_first_cuda_work_of_a_thread_through_the_binding():
     torch.cuda.synchronize()
     assert torch.equal(y, R.rib_linear_fwd(x, w)[0])
     assert torch.equal(got[0], R.rib_window_attn_fwd(qkv, 16, 0, rank=0)[0])
+
+
+# pairs of shapes that run as one instance of a kernel: one and sixteen warps of
+# the norm's pipelines, column tiles of 64 and 256, rings of two and four chunks
+PAIRS = {"norm": (_norm, (4, 192), (20000, 192)), "linear": (_linear, (100, 64, 64), (100, 64, 2048)),
+         "feed-forward": (_ffn, (800, 64, 64), (800, 256, 64))}
+
+
+@pytest.mark.parametrize("name", PAIRS)
+def test_two_threads_at_once(name):
+    """At shapes whose kernels take different amounts of shared memory: every call
+    succeeds and gives what it gives alone."""
+    make, *shapes = PAIRS[name]
+    calls = [make(*s, seed=11 + 7 * i) for i, s in enumerate(shapes)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    alone = []
+    for fn, args, _, y in calls:
+        assert fn(*args, torch.cuda.current_stream().cuda_stream) == 0
+        alone.append(y.clone())
+        y.zero_()
+    torch.cuda.synchronize()
+    codes = [set(), set()]
+    gate = threading.Barrier(2)
+
+    def run(i):
+        fn, args, _, _ = calls[i]
+        st = streams[i].cuda_stream
+        gate.wait()
+        for k in range(CALLS):
+            codes[i].add(fn(*args, st))
+            if k % 500 == 499:   # bounds what is queued
+                streams[i].synchronize()
+
+    every = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(every)
+    torch.cuda.synchronize()
+    assert codes == [{0}, {0}]
+    assert R.rib_last_status()[0] == 0
+    for (_, _, _, y), ref in zip(calls, alone):
+        assert torch.equal(y, ref)

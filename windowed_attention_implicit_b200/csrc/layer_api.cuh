@@ -44,7 +44,6 @@ int launch(void (*kernel)(Args...), dim3 grid, int block, size_t smem, cudaStrea
 
 constexpr int kMaxChannels = 65536;
 constexpr int kMaxRows = 1 << 30;
-constexpr size_t kSmemMax = 227 * 1024;
 
 int check_product(int rows, int K, int N) {
   if (rows < 0 || K <= 0 || N <= 0) return RIB_ERR_ARG;
@@ -426,7 +425,7 @@ int ln_launch_row(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st)
     return launch(ln_row_fwd_kernel<T, V, NV, CTA>, dim3(n.grid), kLnThreads, 0, st, 1, p);
   }
   const size_t smem = CTA || !p.part ? 0 : (size_t)kLnWarps * 2 * p.C * 4;
-  int rc = set_smem(ln_row_bwd_kernel<T, V, NV, CTA>, smem);
+  int rc = set_smem(ln_row_bwd_kernel<T, V, NV, CTA>, smem, kSmemBesideStatic);
   if (rc) return rc;
   TraceScope ts(K_LN_BWD, st);
   return launch(ln_row_bwd_kernel<T, V, NV, CTA>, dim3(n.grid), kLnThreads, smem, st, 1, p);
@@ -438,7 +437,7 @@ int ln_launch_async(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t s
   if constexpr (V != 1 || NV < 16) {   // plan_ln
     if (bwd) kernel = ln_async_kernel<T, V, NV, L, true>;
   }
-  int rc = set_smem(kernel, n.smem);
+  int rc = set_smem(kernel, n.smem, kSmemBesideStatic);
   if (rc) return rc;
   LnBlocks q = n.q;
   q.wait_limit_ns = g_wait_limit_ns;

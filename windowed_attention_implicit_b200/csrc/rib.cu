@@ -217,10 +217,20 @@ int launch_status() {
   return cudaGetLastError() == cudaSuccess ? RIB_OK : RIB_ERR_CUDA;
 }
 
+// Dynamic shared memory that a block may have, beside up to 1 KB of static
+// shared memory for the kernels that have some.
+constexpr size_t kSmemMax = 227 * 1024, kSmemBesideStatic = kSmemMax - 1024;
+
+// Lets a kernel be launched with `bytes` of dynamic shared memory.  The limit
+// belongs to the function, not to the launch that follows: every call sets it
+// to the same value, all there is, so that host threads calling at once, at
+// shapes that need more and less, never lower it between another's call here and
+// its launch.
 template <typename K>
-int set_smem(K kernel, size_t bytes) {
+int set_smem(K kernel, size_t bytes, size_t most = kSmemMax) {
+  if (bytes > most) return RIB_ERR_UNSUPPORTED;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes)) == cudaSuccess
+                              static_cast<int>(most)) == cudaSuccess
              ? RIB_OK
              : RIB_ERR_CUDA;
 }
@@ -1207,7 +1217,7 @@ static int window_copy(const void* src, void* dst, int B, int H, int W, int C, i
   p.gather = gather;
   p.wait_limit_ns = g_wait_limit_ns;
   const size_t smem = 2ull * p.box_bytes + 1024;
-  if ((rc = set_smem(window_copy_kernel, smem))) return rc;
+  if ((rc = set_smem(window_copy_kernel, smem, kSmemBesideStatic))) return rc;
   dim3 grid((M / 8) * (M / 8), nW, B);
   TraceScope ts(K_COPY, static_cast<cudaStream_t>(stream));
   window_copy_kernel<<<grid, 32, smem, static_cast<cudaStream_t>(stream)>>>(mx, mw, p);
