@@ -293,26 +293,40 @@ constexpr float kLog2e = 1.4426950408889634f;
 // the accuracy allows.
 //
 // gelu(z) = z Phi(z) = max(z, 0) - t Q, t = |z|, Q = erfc(t / sqrt 2) / 2 =
-// e^(-t^2/2) R(t): one exponential, and R by a polynomial on [0, 6]
-// (fit_gelu_poly.py: |dQ| <= 0.081 (2^-12 Q + 1e-7), far below the result's
-// bf16 step; t is capped at 6 there and in its product with Q, whose value
-// beyond is below 1e-9).  The coefficients' signs are those of a polynomial
-// in -t.
-__device__ __forceinline__ uint64_t gelu_pair(uint64_t z) {
-  const float z0 = lo2(z), z1 = hi2(z);
-  const uint64_t nt = pk2(fmaxf(-fabsf(z0), -6.f), fmaxf(-fabsf(z1), -6.f));
-  const uint64_t arg = fmul2(fmul2(z, pk2(-0.5f * kLog2e, -0.5f * kLog2e)), z);
-  const uint64_t e = pk2(ex2_approx(lo2(arg)), ex2_approx(hi2(arg)));
-  uint64_t p = ffma2(nt, pk2(1.58075409e-06f, 1.58075409e-06f), pk2(4.28002786e-05f, 4.28002786e-05f));
-  p = ffma2(p, nt, pk2(0.000506665034f, 0.000506665034f));
-  p = ffma2(p, nt, pk2(0.00349101517f, 0.00349101517f));
-  p = ffma2(p, nt, pk2(0.0158246104f, 0.0158246104f));
-  p = ffma2(p, nt, pk2(0.0510843322f, 0.0510843322f));
-  p = ffma2(p, nt, pk2(0.125478402f, 0.125478402f));
-  p = ffma2(p, nt, pk2(0.247342557f, 0.247342557f));
-  p = ffma2(p, nt, pk2(0.398556024f, 0.398556024f));
-  p = ffma2(p, nt, pk2(0.499990076f, 0.499990076f));
-  return ffma2(fmul2(p, e), nt, pk2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
+// e^(-t^2/2) R(t), and R = k P(k) with k = 1 / (1 + c t) and a polynomial P
+// (fit_gelu_poly.py).  The fit is relative, 4.6e-6, and holds as far as Q is a
+// normal number: for z < 0 the result is -t Q itself, and its bf16 step is
+// relative.  (A polynomial in t on [0, 6] with absolute bounds left up to 4 % of
+// that result there.)  One reciprocal serves four elements, 1/a = b c d / (a b c
+// d), with t capped at 16, where the exponential is 0, so that the factors lie
+// within [1, 6] and an infinite z gives no NaN.
+__device__ __forceinline__ void gelu_quad(uint64_t& z01, uint64_t& z23) {
+  const float z[4] = {lo2(z01), hi2(z01), lo2(z23), hi2(z23)};
+  float m[4];   // -t
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(-fabsf(z[i]), -16.f);
+  const uint64_t m01 = pk2(m[0], m[1]), m23 = pk2(m[2], m[3]);
+  const uint64_t c = pk2(-0.31f, -0.31f), one = pk2(1.f, 1.f);
+  const uint64_t a01 = ffma2(m01, c, one), a23 = ffma2(m23, c, one);
+  const float p01 = lo2(a01) * hi2(a01), p23 = lo2(a23) * hi2(a23);
+  const float r = rcp_approx(p01 * p23);
+  const float r01 = r * p23, r23 = r * p01;   // 1 / (a0 a1), 1 / (a2 a3)
+  const uint64_t k01 = fmul2(pk2(hi2(a01), lo2(a01)), pk2(r01, r01));
+  const uint64_t k23 = fmul2(pk2(hi2(a23), lo2(a23)), pk2(r23, r23));
+  const uint64_t h = pk2(-0.5f * kLog2e, -0.5f * kLog2e);
+  const uint64_t x01 = fmul2(fmul2(z01, h), z01), x23 = fmul2(fmul2(z23, h), z23);
+  const uint64_t e01 = pk2(ex2_approx(lo2(x01)), ex2_approx(hi2(x01)));
+  const uint64_t e23 = pk2(ex2_approx(lo2(x23)), ex2_approx(hi2(x23)));
+  auto poly = [](uint64_t k) {
+    uint64_t p = ffma2(k, pk2(-0.0739237592f, -0.0739237592f), pk2(0.180433989f, 0.180433989f));
+    p = ffma2(p, k, pk2(0.0157634765f, 0.0157634765f));
+    p = ffma2(p, k, pk2(0.133419752f, 0.133419752f));
+    p = ffma2(p, k, pk2(0.120443746f, 0.120443746f));
+    p = ffma2(p, k, pk2(0.123860478f, 0.123860478f));
+    return fmul2(p, k);
+  };
+  z01 = ffma2(fmul2(poly(k01), e01), m01, pk2(fmaxf(z[0], 0.f), fmaxf(z[1], 0.f)));
+  z23 = ffma2(fmul2(poly(k23), e23), m23, pk2(fmaxf(z[2], 0.f), fmaxf(z[3], 0.f)));
 }
 
 // silu(z) = z / (1 + e^-z) = max(z, 0) - |z| f with E = e^-|z| <= 1 and f = E / (1
@@ -348,31 +362,31 @@ __device__ __forceinline__ void silu_quad(uint64_t& z01, uint64_t& z23) {
 template <int ACT>
 __device__ __forceinline__ void act_quad(uint64_t& z01, uint64_t& z23) {
   if constexpr (ACT == kActGelu) {
-    z01 = gelu_pair(z01);
-    z23 = gelu_pair(z23);
+    gelu_quad(z01, z23);
   } else if constexpr (ACT == kActSilu) {
     silu_quad(z01, z23);
   }
 }
 
 // act(z) and act'(z) for the backward, to fp32 accuracy (the bias gradients
-// are fp32 sums of what is formed from them).  gelu: with k = 1 / (1 + p t /
-// sqrt 2), Abramowitz and Stegun's formula 7.1.26 gives 2 Q = (a1 k + ... +
-// a5 k^5) e^(-t^2/2) to 1.5e-7; the slope is Phi + z phi, from the same
-// exponential.  (|z| is capped in products with Q and the exponential, whose
-// values there are 0, so that an infinite z gives no NaN.)
+// are fp32 sums of what is formed from them), and the value for few rows.
+// gelu: as above with a longer polynomial, Q to 4e-7 of itself; the slope is Phi +
+// z phi, from the same exponential.
 template <int ACT>
 __device__ __forceinline__ void act_both(float z, float& a, float& da) {
   if constexpr (ACT == kActGelu) {
-    const float k = rcp_approx(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+    const float cap = fminf(fmaxf(z, -16.f), 16.f), t = fabsf(cap);
+    const float k = rcp_approx(fmaf(t, 0.3f, 1.f));
     const float e = ex2_approx(z * z * (-0.5f * kLog2e));
-    float p = fmaf(k, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    p = fmaf(p, k, 0.5f * 1.421413741f);
-    p = fmaf(p, k, 0.5f * -0.284496736f);
-    p = fmaf(p, k, 0.5f * 0.254829592f);
+    float p = fmaf(k, 0.0357484072f, -0.157488391f);
+    p = fmaf(p, k, 0.206804186f);
+    p = fmaf(p, k, -0.0540565774f);
+    p = fmaf(p, k, 0.128734082f);
+    p = fmaf(p, k, 0.0998697057f);
+    p = fmaf(p, k, 0.12075948f);
+    p = fmaf(p, k, 0.11962904f);
     const float q = p * k * e;
-    const float cap = fminf(fmaxf(z, -1e4f), 1e4f);
-    a = fmaf(-fabsf(cap), q, fmaxf(z, 0.f));
+    a = fmaf(-t, q, fmaxf(z, 0.f));
     da = fmaf(cap, 0.3989422804f * e, z > 0.f ? 1.f - q : q);
   } else if constexpr (ACT == kActSilu) {
     const float s = rcp_approx(1.f + ex2_approx(-kLog2e * z));
