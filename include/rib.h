@@ -379,7 +379,8 @@ int rib_window_attn_bwd_masked(const void* qkv, const void* out, const void* dou
 #define RIB_DTYPE_BF16 0
 #define RIB_DTYPE_F32  1
 
-/* Activations: none, gelu(z) = z Phi(z) (erf form), silu(z) = z / (1 + e^-z). */
+/* Activations: none, gelu(z) = z Phi(z) (erf form), silu(z) = z / (1 + e^-z); at
+ * infinite z the limits of value and slope (0 and 0, or infinity and 1). */
 #define RIB_ACT_NONE 0
 #define RIB_ACT_GELU 1
 #define RIB_ACT_SILU 2

@@ -111,3 +111,23 @@ def test_slope_in_its_tail(act, rows):
     err = np.abs(_np(g["dx"]) - want)
     # rounded as dz and, unchanged by the product with ones and zeros, as dx
     assert (err <= H * (np.abs(want) + APPROX * parts) + APPROX * parts).all()
+
+
+@pytest.mark.parametrize("rows", [1, 4, 8, 9, 300])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_infinite_values_give_the_limits(act, rows):
+    """An infinite pre-activation, here from the bias: 0 and infinity, and slopes
+    0 and 1, however many rows there are; the other columns stay as they are."""
+    inf = float("inf")
+    eye = torch.eye(16, dtype=bf).cuda()
+    x = torch.linspace(-3, 3, rows * 16).to(bf).view(rows, 16).cuda()
+    b = torch.zeros(16, device="cuda")
+    clean, _ = R.rib_linear_fwd(x, eye, b, act=act)
+    b[3], b[8] = -inf, inf
+    y, pre = R.rib_linear_fwd(x, eye, b, act=act, save_pre=True)
+    g = R.rib_linear_bwd(x, eye, torch.ones_like(x), act=act, pre=pre)
+    _done()
+    rest = [i for i in range(16) if i not in (3, 8)]
+    assert (y[:, 3] == 0).all() and (y[:, 8] == inf).all() and torch.equal(y[:, rest], clean[:, rest])
+    assert (g["dx"][:, 3] == 0).all() and (g["dx"][:, 8] == 1).all() and torch.isfinite(g["dx"]).all()
+    assert g["db"][3] == 0 and g["db"][8] == rows

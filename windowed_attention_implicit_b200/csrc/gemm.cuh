@@ -389,9 +389,11 @@ __device__ __forceinline__ void act_both(float z, float& a, float& da) {
     a = fmaf(-t, q, fmaxf(z, 0.f));
     da = fmaf(cap, 0.3989422804f * e, z > 0.f ? 1.f - q : q);
   } else if constexpr (ACT == kActSilu) {
+    // z is bounded in its products with what vanishes there, so that an infinite
+    // one gives the limits (0 and 0, or infinity and 1), as silu_quad does
     const float s = rcp_approx(1.f + ex2_approx(-kLog2e * z));
-    a = z * s;
-    da = fmaf(a, 1.f - s, s);
+    a = fmaxf(z, -1e4f) * s;
+    da = fmaf(fminf(a, 1e4f), 1.f - s, s);
   } else {
     a = z;
     da = 1.f;
