@@ -760,9 +760,9 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
         }
 #pragma unroll
         for (int k = 0; k < RR; ++k) {
-          // dx = r g + (-r^2 m2) (x - mean) + (dres - r m1)
-          const uint64_t kg = ln_both(rs[k]), kx = ln_both(-rs[k] * rs[k] * m2[k]),
-                         k1 = ln_both(-rs[k] * m1[k]);
+          // dx = r (g - m1 - (r m2) (x - mean)) + dres: r m2, not r^2 m2, which is beyond
+          // fp32 for rows of spread below 1e-19
+          const uint64_t kg = ln_both(rs[k]), kx = ln_both(-rs[k] * m2[k]), k1 = ln_both(-m1[k]);
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             if (!in_row[k] || ln_column<V, L>(i, j, 0, 0) >= C) continue;
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
             }
 #pragma unroll
             for (int e = 0; e < P; ++e)
-              a[e] = ffma2(kg, gd[k][i][e], ffma2(kx, xc[k][i][e], fadd2(a[e], k1)));
+              a[e] = ffma2(kg, ffma2(kx, xc[k][i][e], fadd2(gd[k][i][e], k1)), a[e]);
             LP::put(d0 + off[k], i, j, C, a);
           }
         }
