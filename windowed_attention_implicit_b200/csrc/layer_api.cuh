@@ -365,9 +365,10 @@ LnPlan plan_ln(int rows, int C, int es, bool bwd, bool aligned, int sms) {
   const int arrays = bwd ? 3 : 1;   // also without dres: the sums then run in the same order
   const int v = 16 / es;
   n.vec = aligned && C % v == 0 ? v : 1;
-  // (the backward of more than 768 single elements spills there: 60000 x 1001 of
-  // bf16 260 us, 213 by row kernels; at 601 116)
-  if (aligned && C <= 1024 && !(bwd && n.vec == 1 && C > 768)) {
+  // (also the backward of more than 768 single elements of bf16, though it spills:
+  // 60000 x 777 204 us, by the row kernels 419; x 1001 259 for 508; of fp32 up to
+  // 780, where the stages still fit, 777 227 for 313)
+  if (aligned && C <= 1024) {
     const int vecs = C / n.vec;
     // as few lanes per row as keep four vectors (or pairs of single elements) a
     // lane (backward of 122931 x 10 15 us, with all 32 lanes 72; x 100 57 for 77)
@@ -433,10 +434,7 @@ int ln_launch_row(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st)
 
 template <typename T, int V, int NV, int L>
 int ln_launch_async(const LnParams& p, const LnPlan& n, bool bwd, cudaStream_t st) {
-  auto kernel = ln_async_kernel<T, V, NV, L, false>;
-  if constexpr (V != 1 || NV < 16) {   // plan_ln
-    if (bwd) kernel = ln_async_kernel<T, V, NV, L, true>;
-  }
+  auto kernel = bwd ? ln_async_kernel<T, V, NV, L, true> : ln_async_kernel<T, V, NV, L, false>;
   int rc = set_smem(kernel, n.smem, kSmemBesideStatic);
   if (rc) return rc;
   LnBlocks q = n.q;

@@ -24,9 +24,9 @@
 // 333 channels, backward of 9217 rows 22 us: 49 MB, but single elements in
 // shared memory bound it, not HBM.
 //
-// ln_row_*_kernel (wider rows, the backward of more than 768 channels that are
-// not whole vectors, or pointers off a 16-byte address): a group of threads (a
-// CTA above 1024 channels, else a warp) holds a row in registers.
+// ln_row_*_kernel (wider rows, the fp32 backward of more than 780 channels
+// that are not whole vectors, or pointers off a 16-byte address): a group of
+// threads (a CTA above 1024 channels, else a warp) holds a row in registers.
 #pragma once
 
 #include <cuda_bf16.h>
