@@ -370,8 +370,10 @@ int rib_window_attn_bwd_masked(const void* qkv, const void* out, const void* dou
  *
  * Common to all of them: rows == 0 is a valid no-op (pointers not looked at)
  * except that weight gradients, then empty sums, are zeroed; outputs must not
- * overlap inputs unless an argument says so; sums over rows go through
- * partials added in a fixed order, so repeated calls give the same bits.
+ * overlap inputs or one another (RIB_ERR_ARG where the result would suffer),
+ * except that one may take an input's place, element for element, where an
+ * argument says so; sums over rows go through partials added in a fixed order,
+ * so repeated calls give the same bits.
  * The products take bf16 operands with fp32 accumulation and every channel
  * count a multiple of 8 (a 16-byte row pitch), at most 65536, else
  * RIB_ERR_UNSUPPORTED; rows may be any number up to 2^30.
@@ -410,7 +412,7 @@ int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* g
  *
  *   x, dy, dres, dx : [rows][C] of `dtype`; dres (a second gradient of x, as
  *            the residual path's, added before the one rounding) may be NULL;
- *            dx may be dy or dres
+ *            dx may be x, dy or dres
  *   mean, rstd : from rib_layer_norm_fwd
  *   gamma  : as given to the forward (NULL: ones)
  *   dgamma, dbeta : out, fp32 [C]; either may be NULL (not wanted)
@@ -471,7 +473,7 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
  *   w_in   : bf16 [2][hidden][C], Wg then Wu;  b_in : fp32 [2][hidden] or NULL
  *   w_out  : bf16 [C][hidden];                 b_out : fp32 [C] or NULL
  *   residual : bf16 [rows][C] or NULL
- *   y      : out, bf16 [rows][C]; may be residual
+ *   y      : out, bf16 [rows][C]; may be residual or x
  *   workspace : device, >= rib_gated_ffn_fwd_workspace() bytes (h, where two
  *            products are faster than one kernel; 0: may be NULL) on the current
  *            device, 256-byte aligned; to be asked for each number of rows, fewer

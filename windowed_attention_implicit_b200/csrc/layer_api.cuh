@@ -349,6 +349,30 @@ bool aligned16_all(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// ---------------------------------------------------------------- overlaps
+
+struct Span {
+  const void* p;   // may be null
+  size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// An output on memory that the call still reads or writes otherwise.
+bool clash(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (overlap(out, o)) return true;
+  return false;
+}
+// The same where the output may take the other's place, element for element.
+bool clash_unless_same(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (out.p != o.p && overlap(out, o)) return true;
+  return false;
+}
+
 // ---------------------------------------------------------------- layer norm
 
 // How one call runs: the asynchronous kernel's vector width, vectors per
@@ -688,6 +712,11 @@ int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* g
   if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(gamma, 4) || !aligned_to(beta, 4) ||
       !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return RIB_ERR_ALIGN;
+  const size_t map = es * rows * C, row = 4ull * rows, col = 4ull * C;
+  if (clash_unless_same({y, map}, {{x, map}}) || clash({y, map}, {{gamma, col}, {beta, col}}) ||
+      clash({mean, row}, {{x, map}, {y, map}, {rstd, row}, {gamma, col}, {beta, col}}) ||
+      clash({rstd, row}, {{x, map}, {y, map}, {gamma, col}, {beta, col}}))
+    return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   LnParams p{};
@@ -727,6 +756,11 @@ int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C
   if (sums && (rc = check_workspace(workspace, workspace_bytes,
                                     rib_layer_norm_bwd_workspace(rows, C))))
     return rc;
+  const size_t map = es * rows * C, row = 4ull * rows, col = 4ull * C;
+  if (clash_unless_same({dx, map}, {{x, map}, {dy, map}, {dres, map}}) ||
+      clash({dx, map}, {{mean, row}, {rstd, row}, {gamma, col}, {dgamma, col}, {dbeta, col}}) ||
+      clash({dgamma, col}, {{dbeta, col}}))
+    return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   LnParams p{};
@@ -749,13 +783,18 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (rows == 0) return RIB_OK;
   if (!x || !w || !y) return RIB_ERR_ARG;
   if (!aligned16_all({x, w, bias, residual, pre, y})) return RIB_ERR_ALIGN;
-  // other tiles still read x, and the residual after pre is written
-  if (y == x || pre == x || pre == y || (pre && pre == residual)) return RIB_ERR_ARG;
+  // other tiles still read x and the weights, and the residual after pre is written
+  const size_t in = 2ull * rows * K, out = 2ull * rows * N, wts = 2ull * N * K, col = 4ull * N;
+  if (clash({y, out}, {{x, in}, {pre, out}}) || clash_unless_same({y, out}, {{residual, out}}) ||
+      clash({pre, out}, {{x, in}, {residual, out}}))
+    return RIB_ERR_ARG;
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  if (clash({y, out}, {{w, wts}, {bias, col}}) || clash({pre, out}, {{w, wts}, {bias, col}}))
+    return RIB_ERR_ARG;
   if (few_rows_win(rows, K, N))
     return launch_few<false>(act, x, w, bias, residual, pre, y, rows, N, K,
                              static_cast<cudaStream_t>(stream));
-  int sms = 0;
-  if ((rc = device_sms(&sms))) return rc;
   const GemmPlan g = plan_gemm(kLinear, rows, N, K, residual != nullptr, sms);
   return launch_gemm_act<kLinear>(act, K_LINEAR, g, x, w, bias, residual, pre, y, rows, N, K,
                                   static_cast<cudaStream_t>(stream));
@@ -780,9 +819,16 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
     return zero_async(db, (size_t)N * 4, st);
   }
   if (!dy || (dx && !w) || (dw && !x) || (act != RIB_ACT_NONE && !pre)) return RIB_ERR_ARG;
-  if (dx && (dx == dy || dx == x)) return RIB_ERR_ARG;   // both are read after dx is written
+  const size_t in = 2ull * rows * K, out = 2ull * rows * N, wts = 2ull * N * K,
+               grad = dtype_bytes(dw_dtype) * N * K, col = 4ull * N;
+  // x and dy are read after dx is written
+  if (clash({dx, in}, {{dy, out}, {x, in}}) || clash_unless_same({dx, in}, {{dx_add, in}}))
+    return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
+  if (clash({dx, in}, {{w, wts}}) || clash({dw, grad}, {{x, in}, {dy, out}, {dx, in}}) ||
+      clash({db, col}, {{x, in}, {dy, out}, {dx, in}, {dw, grad}, {w, wts}, {dx_add, in}}))
+    return RIB_ERR_ARG;
   const LinearBwdWs L = linear_bwd_ws(rows, K, N, act, sms);
   if ((rc = check_workspace(workspace, workspace_bytes, L.total))) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -840,8 +886,12 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   if ((rc = check_workspace(workspace, workspace_bytes,
                             rib_gated_ffn_fwd_workspace(rows, C, hidden))))
     return rc;
+  const size_t map = 2ull * rows * C, wts = 2ull * hidden * C, col = 4ull * hidden;
+  if (clash_unless_same({y, map}, {{x, map}, {residual, map}})) return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
+  if (clash({y, map}, {{w_in, 2 * wts}, {b_in, 2 * col}, {w_out, wts}, {b_out, 4ull * C}}))
+    return RIB_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows_win(rows, C, 2 * hidden)) {
     if ((rc = launch_few<true>(act, x, w_in, b_in, nullptr, nullptr, workspace, rows,
@@ -892,9 +942,21 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
     return zero_async(db_out, (size_t)C * 4, st);
   }
   if (!x || !w_in || !w_out || !dy || !dx) return RIB_ERR_ARG;
-  if (dx == x || dx == dy) return RIB_ERR_ARG;   // both are read after dx is written
+  const size_t map = 2ull * rows * C, wts = 2ull * hidden * C, grad = es * hidden * C,
+               col = 4ull * hidden;
+  // x and dy are read after dx is written
+  if (clash({dx, map}, {{x, map}, {dy, map}}) || clash_unless_same({dx, map}, {{dx_add, map}}))
+    return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
+  const Span maps[3] = {{x, map}, {dy, map}, {dx, map}};
+  const Span sums[4] = {{dw_in, 2 * grad}, {dw_out, grad}, {db_in, 2 * col}, {db_out, 4ull * C}};
+  if (clash({dx, map}, {{w_in, 2 * wts}})) return RIB_ERR_ARG;
+  for (int i = 0; i < 4; ++i) {
+    if (clash(sums[i], {maps[0], maps[1], maps[2]})) return RIB_ERR_ARG;
+    for (int k = 0; k < i; ++k)
+      if (overlap(sums[i], sums[k])) return RIB_ERR_ARG;
+  }
   const FfnBwdWs L = ffn_bwd_ws(rows, C, hidden, sms);
   if ((rc = check_workspace(workspace, workspace_bytes, L.total))) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
