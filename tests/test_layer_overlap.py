@@ -110,3 +110,16 @@ def test_outputs_in_the_place_of_inputs(rows):
     torch.cuda.synchronize()
     assert torch.equal(a, plain) and torch.equal(b, res)
     assert R.rib_last_status()[0] == 0
+
+
+def test_no_rows_looks_at_no_map():
+    """A map without rows may have any address, an odd one too."""
+    odd = FAKE + 1
+    assert ln_fwd(rows=0, x=odd, y=odd, gamma=odd) == _abi.RIB_OK
+    assert ln_bwd(rows=0, x=odd, dy=odd, dx=odd, mean=odd, dgamma=None, dbeta=None) == _abi.RIB_OK
+    assert lin_fwd(rows=0, x=odd, w=odd, y=odd) == _abi.RIB_OK
+    assert lin_bwd(rows=0, x=odd, w=odd, pre=odd, dy=odd, dx_add=odd, dx=odd, dw=None, db=None) == _abi.RIB_OK
+    assert ffn_fwd(rows=0, x=odd, y=odd, residual=odd) == _abi.RIB_OK
+    # the sums are written: refused where they lie, before anything is
+    assert lin_bwd(rows=0, x=odd, dw=odd, db=None) == _abi.RIB_ERR_ALIGN
+    assert ffn_bwd(rows=0, x=odd, dy=odd, dx=odd, dw_in=odd) == _abi.RIB_ERR_ALIGN

@@ -812,12 +812,13 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
   int rc = check_product(rows, K, N);
   if (rc || (rc = check_act(act))) return rc;
   if (dw_dtype != RIB_DTYPE_BF16 && dw_dtype != RIB_DTYPE_F32) return RIB_ERR_ARG;
-  if (!aligned16_all({x, w, pre, dy, dx_add, dx, dw, db})) return RIB_ERR_ALIGN;
+  if (!aligned16_all({dw, db})) return RIB_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (rows == 0) {   // empty sums
+  if (rows == 0) {   // empty sums; the maps are not looked at
     if ((rc = zero_async(dw, (size_t)N * K * dtype_bytes(dw_dtype), st))) return rc;
     return zero_async(db, (size_t)N * 4, st);
   }
+  if (!aligned16_all({x, w, pre, dy, dx_add, dx})) return RIB_ERR_ALIGN;
   if (!dy || (dx && !w) || (dw && !x) || (act != RIB_ACT_NONE && !pre)) return RIB_ERR_ARG;
   const size_t in = 2ull * rows * K, out = 2ull * rows * N, wts = 2ull * N * K,
                grad = dtype_bytes(dw_dtype) * N * K, col = 4ull * N;
@@ -931,16 +932,16 @@ int rib_gated_ffn_bwd(const void* x, int rows, int C, int hidden, const void* w_
   if (rc || (rc = check_act(act))) return rc;
   if (dw_dtype != RIB_DTYPE_BF16 && dw_dtype != RIB_DTYPE_F32) return RIB_ERR_ARG;
   if (!dw_in || !dw_out) return RIB_ERR_ARG;
-  if (!aligned16_all({x, w_in, b_in, w_out, dy, dx_add, dx, dw_in, db_in, dw_out, db_out}))
-    return RIB_ERR_ALIGN;
+  if (!aligned16_all({dw_in, db_in, dw_out, db_out})) return RIB_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t es = dtype_bytes(dw_dtype);
-  if (rows == 0) {   // empty sums
+  if (rows == 0) {   // empty sums; the maps are not looked at
     if ((rc = zero_async(dw_in, 2 * es * hidden * C, st))) return rc;
     if ((rc = zero_async(db_in, (size_t)hidden * 8, st))) return rc;
     if ((rc = zero_async(dw_out, es * C * hidden, st))) return rc;
     return zero_async(db_out, (size_t)C * 4, st);
   }
+  if (!aligned16_all({x, w_in, b_in, w_out, dy, dx_add, dx})) return RIB_ERR_ALIGN;
   if (!x || !w_in || !w_out || !dy || !dx) return RIB_ERR_ARG;
   const size_t map = 2ull * rows * C, wts = 2ull * hidden * C, grad = es * hidden * C,
                col = 4ull * hidden;
