@@ -478,7 +478,8 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
  *            products are faster than one kernel; 0: may be NULL) on the current
  *            device, 256-byte aligned; to be asked for each number of rows, fewer
  *            rows can need more
- * h is rounded to bf16, as the second product takes it; y once.  hidden <= 32768.
+ * h is rounded to bf16 where the tensor cores take it (not for a few rows, whose
+ * products run without them); y once.  hidden <= 32768.
  * ------------------------------------------------------------------------ */
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden);
 int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_in,

@@ -54,3 +54,21 @@ def test_many_calls_give_the_same_bits():
         bad += (y != want).sum()
     _done()
     assert int(bad) == 0
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "none"])
+@pytest.mark.parametrize("rows,C,Hd", [(1, 1024, 2816), (2, 16, 1512), (1, 8, 8), (3, 96, 384), (5, 192, 768),
+                                       (8, 64, 256)])
+def test_few_rows_keep_h_in_fp32(rows, C, Hd, act):
+    """Without the tensor cores h is not rounded: what separates y from the formula
+    is y's own rounding, fp32 sums of at most (C + Hd) terms and the activation's
+    error, which the tiled form's bounds have beside a rounding of every h."""
+    x, wi, bi, wo, bo, r = _ffn_case(rows, C, Hd)
+    y = R.rib_gated_ffn_fwd(x.cuda(), _ffn_dev(wi, bi, wo, bo), act=act, residual=r.cuda())
+    _done()
+    ref = O.gated_ffn_fwd(x, wi, bi, wo, bo, act, r)
+    *_, h, _, _, _, eh = _ffn_inner(x, wi, bi, act)
+    eh = (eh - H * np.abs(h)) / (1 + H)          # without the rounding of h
+    W = np.abs(_np(wo)).T
+    e = eh @ W + _mma(Hd) * (np.abs(h) @ W + np.abs(_np(bo)) + np.abs(_np(r)))
+    _within(y, ref, e + H * (np.abs(ref) + e), "y")

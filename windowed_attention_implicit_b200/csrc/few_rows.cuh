@@ -1,7 +1,11 @@
 // few_rows.cuh -- projections of up to eight rows (single tokens), forward.
 //
 //   linear   y = act(x W^T + bias) + residual
-//   gated    y = act(x Wg^T + bg) (x Wu^T + bu)
+//   gated    h = act(x Wg^T + bg) (x Wu^T + bu)
+//
+// The gated form is the first half of the feed-forward block; its h goes to the
+// second product in fp32, since no tensor core wants it in bf16 here and it is
+// read from L2 (two rows of 16 channels, 1512 hidden: error 2.7e-3 with h in bf16).
 //
 // With so few rows a product is one read of the weights, and a tensor-core
 // tile of 128 rows would spend its time on tile set-up: here a warp takes two
@@ -20,9 +24,11 @@ constexpr int kFewThreads = 128;
 constexpr int G_FEW_W = 177, G_FEW_X = 178, G_FEW_OUT = 179;
 
 struct FewParams {
-  const __nv_bfloat16 *x, *w, *residual;
+  const void* x;              // bf16, or fp32 (X32)
+  const __nv_bfloat16 *w, *residual;
   const float* bias;
-  __nv_bfloat16 *pre, *y;
+  __nv_bfloat16* pre;
+  void* y;                    // bf16, or fp32 (GATED)
   int rows, K, N;
 };
 
@@ -35,9 +41,22 @@ __device__ __forceinline__ void few_unpack(const uint4& r, float (&f)[8]) {
   }
 }
 
+// Eight elements of x from element `at`
+template <bool X32>
+__device__ __forceinline__ void few_load(const void* x, size_t at, float (&f)[8]) {
+  if constexpr (X32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    few_unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at)), f);
+  }
+}
+
 // R: rows of x held (the first p.rows of them are real).
 // grid ceil(outputs / (2 or 1 per warp) / 4), block kFewThreads.
-template <int R, int ACT, bool GATED>
+template <int R, int ACT, bool GATED, bool X32>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
   constexpr int U = R <= 2 ? 4 : 2;   // 16-byte pieces of each weight row in flight
   pdl_wait();
@@ -73,7 +92,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
         const size_t at = static_cast<size_t>(r) * p.K + k;
         if (r >= p.rows || !rib_guard(at + 7, x_n, G_FEW_X)) continue;
         float fx[8];
-        few_unpack(__ldg(reinterpret_cast<const uint4*>(p.x + at)), fx);
+        few_load<X32>(p.x, at, fx);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           acc[0][r] = fmaf(fa[e], fx[e], acc[0][r]);
@@ -106,12 +125,12 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   float v, slope;
   act_both<ACT>(z, v, slope);
   if constexpr (GATED) {
-    v *= other + (p.bias ? __ldg(p.bias + p.N + n) : 0.f);
+    static_cast<float*>(p.y)[at] = v * (other + (p.bias ? __ldg(p.bias + p.N + n) : 0.f));
   } else {
     if (p.pre) p.pre[at] = __float2bfloat16_rn(z);
     if (p.residual) v += __bfloat162float(p.residual[at]);
+    static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
   }
-  p.y[at] = __float2bfloat16_rn(v);
 }
 
 }  // namespace rib

@@ -214,34 +214,36 @@ bool few_rows_win(int rows, int K, int N) {
   return rows <= 2 || (rows <= kFewRows && (long long)rows * K * N <= 1ll << 24);
 }
 
-template <int ACT, bool GATED>
+template <int ACT, bool GATED, bool X32>
 int launch_few_as(const FewParams& p, cudaStream_t st) {
   const int per_block = kFewThreads / 32 * (GATED ? 1 : 2);
   const int grid = div_up(p.N, per_block);
   TraceScope ts(K_FEW_ROWS, st);
-  if (p.rows == 1)
-    return launch(few_rows_kernel<1, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
-  if (p.rows == 2)
-    return launch(few_rows_kernel<2, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
-  if (p.rows <= 4)
-    return launch(few_rows_kernel<4, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
-  return launch(few_rows_kernel<8, ACT, GATED>, dim3(grid), kFewThreads, 0, st, 1, p);
+  auto kernel = p.rows == 1   ? few_rows_kernel<1, ACT, GATED, X32>
+                : p.rows == 2 ? few_rows_kernel<2, ACT, GATED, X32>
+                : p.rows <= 4 ? few_rows_kernel<4, ACT, GATED, X32>
+                              : few_rows_kernel<8, ACT, GATED, X32>;
+  return launch(kernel, dim3(grid), kFewThreads, 0, st, 1, p);
 }
 
-template <bool GATED>
-int launch_few(int act, const void* x, const void* w, const float* bias, const void* residual,
-               void* pre, void* y, int rows, int N, int K, cudaStream_t st) {
+FewParams few_params(const void* x, const void* w, const float* bias, const void* residual, void* pre,
+                     void* y, int rows, int N, int K) {
   FewParams p{};
-  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.x = x;
   p.w = static_cast<const __nv_bfloat16*>(w);
   p.residual = static_cast<const __nv_bfloat16*>(residual);
   p.bias = bias;
   p.pre = static_cast<__nv_bfloat16*>(pre);
-  p.y = static_cast<__nv_bfloat16*>(y);
+  p.y = y;
   p.rows = rows; p.K = K; p.N = N;
-  return act == RIB_ACT_GELU   ? launch_few_as<kActGelu, GATED>(p, st)
-         : act == RIB_ACT_SILU ? launch_few_as<kActSilu, GATED>(p, st)
-                               : launch_few_as<kActNone, GATED>(p, st);
+  return p;
+}
+
+template <bool GATED>
+int launch_few(int act, const FewParams& p, cudaStream_t st) {
+  return act == RIB_ACT_GELU   ? launch_few_as<kActGelu, GATED, false>(p, st)
+         : act == RIB_ACT_SILU ? launch_few_as<kActSilu, GATED, false>(p, st)
+                               : launch_few_as<kActNone, GATED, false>(p, st);
 }
 
 struct DwPlan {
@@ -793,7 +795,7 @@ int rib_linear_fwd(const void* x, int rows, int K, const void* w, int N, const f
   if (clash({y, out}, {{w, wts}, {bias, col}}) || clash({pre, out}, {{w, wts}, {bias, col}}))
     return RIB_ERR_ARG;
   if (few_rows_win(rows, K, N))
-    return launch_few<false>(act, x, w, bias, residual, pre, y, rows, N, K,
+    return launch_few<false>(act, few_params(x, w, bias, residual, pre, y, rows, N, K),
                              static_cast<cudaStream_t>(stream));
   const GemmPlan g = plan_gemm(kLinear, rows, N, K, residual != nullptr, sms);
   return launch_gemm_act<kLinear>(act, K_LINEAR, g, x, w, bias, residual, pre, y, rows, N, K,
@@ -869,9 +871,8 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden) {
   int sms = 0;
   if (check_ffn(rows, C, hidden)) return 0;
-  if (device_sms(&sms) == RIB_OK && !few_rows_win(rows, C, 2 * hidden) &&
-      fused_wins(rows, C, hidden, sms))
-    return 0;
+  if (few_rows_win(rows, C, 2 * hidden)) return align256((size_t)rows * hidden * 4);
+  if (device_sms(&sms) == RIB_OK && fused_wins(rows, C, hidden, sms)) return 0;
   return align256((size_t)rows * hidden * 2);
 }
 
@@ -895,11 +896,11 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
     return RIB_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows_win(rows, C, 2 * hidden)) {
-    if ((rc = launch_few<true>(act, x, w_in, b_in, nullptr, nullptr, workspace, rows,
-                               hidden, C, st)))
+    if ((rc = launch_few<true>(
+             act, few_params(x, w_in, b_in, nullptr, nullptr, workspace, rows, hidden, C), st)))
       return rc;
-    return launch_few<false>(RIB_ACT_NONE, workspace, w_out, b_out, residual, nullptr, y,
-                             rows, C, hidden, st);
+    return launch_few_as<kActNone, false, true>(
+        few_params(workspace, w_out, b_out, residual, nullptr, y, rows, C, hidden), st);
   }
   if (fused_wins(rows, C, hidden, sms))
     return act == RIB_ACT_GELU   ? launch_fused<kActGelu>(x, w_in, b_in, w_out, b_out, residual, y,
