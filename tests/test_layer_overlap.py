@@ -63,11 +63,12 @@ def test_overlaps_are_refused_before_a_launch():
     g = torch.ones(64, device="cuda")
     y, mean, rstd = R.rib_layer_norm_fwd(x, g)
     _refused(R.rib_layer_norm_fwd, head, g, y=inside)
-    _refused(R.rib_layer_norm_fwd, head, mean=mean, rstd=mean)
+    stats = torch.zeros(96, device="cuda")
+    _refused(R.rib_layer_norm_fwd, head, mean=stats[:64], rstd=stats[32:])
     _refused(R.rib_layer_norm_bwd, head, dy, mean, rstd, dx=inside)
     _refused(R.rib_layer_norm_bwd, x, head, mean, rstd, dx=inside)
     _refused(R.rib_layer_norm_bwd, x, dy, mean, rstd, dres=head, dx=inside)
-    _refused(R.rib_layer_norm_bwd, x, dy, mean, rstd, dgamma=g, dbeta=g)
+    _refused(R.rib_layer_norm_bwd, x, dy, mean, rstd, dgamma=stats[:64], dbeta=stats[32:])
     _refused(R.rib_linear_fwd, head, w, y=inside)
     _refused(R.rib_linear_fwd, x, head, y=inside)
     _refused(R.rib_linear_fwd, x, w, residual=head, y=inside)
@@ -123,3 +124,15 @@ def test_no_rows_looks_at_no_map():
     # the sums are written: refused where they lie, before anything is
     assert lin_bwd(rows=0, x=odd, dw=odd, db=None) == _abi.RIB_ERR_ALIGN
     assert ffn_bwd(rows=0, x=odd, dy=odd, dx=odd, dw_in=odd) == _abi.RIB_ERR_ALIGN
+
+
+@pytest.mark.gpu
+def test_statistics_and_sums_that_nobody_wants_may_share_a_buffer():
+    x, dy = (I.randn((300, 96), seed=i).to(bf).cuda() for i in (1, 2))
+    y, mean, rstd = R.rib_layer_norm_fwd(x)
+    bin_ = torch.empty(300, device="cuda")
+    y2, _, _ = R.rib_layer_norm_fwd(x, mean=bin_, rstd=bin_)
+    g = R.rib_layer_norm_bwd(x, dy, mean, rstd)
+    h = R.rib_layer_norm_bwd(x, dy, mean, rstd, dgamma=bin_[:96], dbeta=bin_[:96])
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(g["dx"], h["dx"])

@@ -716,7 +716,8 @@ int rib_layer_norm_fwd(const void* x, int dtype, int rows, int C, const float* g
     return RIB_ERR_ALIGN;
   const size_t map = es * rows * C, row = 4ull * rows, col = 4ull * C;
   if (clash_unless_same({y, map}, {{x, map}}) || clash({y, map}, {{gamma, col}, {beta, col}}) ||
-      clash({mean, row}, {{x, map}, {y, map}, {rstd, row}, {gamma, col}, {beta, col}}) ||
+      clash({mean, row}, {{x, map}, {y, map}, {gamma, col}, {beta, col}}) ||
+      clash_unless_same({mean, row}, {{rstd, row}}) ||   // one scratch buffer for both will do
       clash({rstd, row}, {{x, map}, {y, map}, {gamma, col}, {beta, col}}))
     return RIB_ERR_ARG;
   int sms = 0;
@@ -761,7 +762,7 @@ int rib_layer_norm_bwd(const void* x, const void* dy, int dtype, int rows, int C
   const size_t map = es * rows * C, row = 4ull * rows, col = 4ull * C;
   if (clash_unless_same({dx, map}, {{x, map}, {dy, map}, {dres, map}}) ||
       clash({dx, map}, {{mean, row}, {rstd, row}, {gamma, col}, {dgamma, col}, {dbeta, col}}) ||
-      clash({dgamma, col}, {{dbeta, col}}))
+      clash_unless_same({dgamma, col}, {{dbeta, col}}))
     return RIB_ERR_ARG;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
