@@ -13,8 +13,8 @@
 // one MMA of 128 columns, then dh), two sets of them in tensor memory; the
 // warp roles are gemm.cuh's with eight epilogue warps.
 //
-// 147456 rows, 192 channels, 384 hidden: 101 us for 453 MB, 4.5 TB/s; the whole
-// backward moves 1290 MB in 262 us, 4.9 TB/s where a plain read gets 5.2.
+// 147456 rows, 192 channels, 384 hidden: 107 us for 453 MB, 4.2 TB/s; the whole
+// backward reads and writes 1190 MB in 262 us, 4.5 TB/s.
 // Nor epilogue (without its arithmetic 117 us for 119, before the following) nor
 // stores (102 without any) bound it but the latency of x and dy, read once per
 // column tile, mostly from L2: so the staging takes 16 columns at a time and a

@@ -17,11 +17,11 @@
 // 8 (a 16-byte row pitch) run without a special case.
 //
 // What bounds the products, and what they take (x and weights in L2 at the small
-// sizes; a plain read of 226 MB takes 43 us here):
+// sizes):
 //   147456 x 192 -> 576         42 us, 226 MB: HBM
 //   147456 x 768 -> 192 (dx)    51 us, 283 MB: HBM
 //   8192 x 4096 -> 4096        172 us, 1.60 PFLOP/s: tensor cores
-//   5003 x 1032 -> 2056         27 us, with gelu and a residual 32: a dozen
+//   5003 x 1032 -> 2056         25 us, with gelu and a residual 30: a dozen
 //     microseconds of set-up, fill and last epilogue, then the tensor cores
 //     (rows of 2064 bytes cost four of them: their 128-byte pieces straddle lines)
 //   8192 x 1024 -> 2 x 2816, gated, gelu  68 us, 1.39 PFLOP/s: tensor cores

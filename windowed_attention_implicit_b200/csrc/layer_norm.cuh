@@ -14,15 +14,17 @@
 // blocks of a few rows.  Rows are contiguous, so a block is one run of bytes
 // whatever the channel count, odd ones included: a bulk copy brings it into
 // one of two or three shared-memory stages, the warp works on it there, writes
-// y (or dx) over x (or dy) and a bulk copy takes it back.  The next blocks are
-// in flight meanwhile, without holding registers, and no warp waits for
-// another.  L lanes hold a row as vectors of V elements, vector j + L i in lane
+// y (or dx) over x (or dy) and a bulk copy takes it back.  With three stages the
+// next blocks are in flight meanwhile, without holding registers; with two (the
+// fp32 backward of 525 to 780 single elements, whose three do not fit) the next
+// block's copy starts when this one's results have left, and its latency shows.
+// No warp waits for another.  L lanes hold a row as vectors of V elements, vector j + L i in lane
 // j, so 192 channels of bf16 use all 32 lanes (four rows of eight lanes, three
 // vectors each) where a lane per vector would idle a quarter of them.
-// Measured, bf16, 192 channels: forward of 294912 rows 40 us (226 MB, 5.7 TB/s),
-// backward of 147456 with a second gradient 41.5 us (226 MB and the sums); fp32,
-// 333 channels, backward of 9217 rows 22 us: 49 MB, but single elements in
-// shared memory bound it, not HBM.
+// Measured, bf16, 192 channels: forward of 294912 rows 38 to 40 us (226 MB, 5.8
+// TB/s), backward of 147456 with a second gradient 41 us (226 MB and the sums);
+// fp32, 333 channels, backward of 9217 rows 20 us for 49 MB: DRAM 22 % and issue 32
+// % busy, so latency at nine warps an SM, single elements by way of shared memory.
 //
 // ln_row_*_kernel (wider rows, the fp32 backward of more than 780 channels
 // that are not whole vectors, or pointers off a 16-byte address): a group of
@@ -168,7 +170,7 @@ __host__ __device__ constexpr int ln_rows() {
 }
 
 // -------------------------------------------------------------- forward
-// grid: a few CTAs per SM (ln_grid), block kLnThreads.
+// grid: a few CTAs per SM (plan_ln), block kLnThreads.
 template <typename T, int V, int NV, bool CTA>
 __global__ void __launch_bounds__(kLnThreads) ln_row_fwd_kernel(const LnParams p) {
   using L = LnVec<T, V>;
@@ -798,8 +800,8 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
       if (lane == 0) {
         if (whole) bulk_store(out + at(b) + head, res + lead + head, whole);
         tma_store_commit();
-        // the stage that the next copies go to (the block before this one's,
-        // or with two stages the one before that) has been read
+        // the stage that the next copies go to, that of the block before this
+        // one, has been read
         bulk_store_wait_read_one();
       }
       __syncwarp();
