@@ -40,3 +40,19 @@ def test_columns_of_h_are_not_overwritten_before_they_are_read():
     gu = fused[fused.index("for (int g = 0; ok && g <= total"):fused.index("pair_commit<2>(&bb.gu_full")]
     assert re.search(r"if \(g >= 2 && !\(ok = warp_wait\(&bb\.y_done\[g & 1\], \(\(g >> 1\) - 1\) & 1,", gu)
     assert re.search(r"pair_umma_ts_steps\(.*?pair_commit<2>\(&bb\.y_done\[g & 1\]\)", fused)
+
+
+def test_dependent_kernels_read_by_coherent_loads():
+    """The layer's kernels are launched before the one they wait for has finished,
+    so what they read is written during their life.  The non-coherent load path
+    (the __ldg intrinsic, the nc loads, const restrict pointers) is for data that
+    is not."""
+    for name in ("layer_norm.cuh", "gemm.cuh", "ffn.cuh", "ffn_fused.cuh", "few_rows.cuh"):
+        code = _code(name)
+        assert "pdl_wait()" in code, name
+        for path in ("__ldg", "ld.global.nc", "__restrict__", "__ldcs", "tex1D"):
+            assert path not in code, (name, path)
+    # the wait orders: loads cannot be moved before it
+    wait = _code("layer_norm.cuh")
+    assert re.search(r'asm volatile\("griddepcontrol\.launch_dependents;\\n\\tgriddepcontrol\.wait;" ::: "memory"\)',
+                     wait)

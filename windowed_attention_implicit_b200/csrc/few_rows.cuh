@@ -46,11 +46,11 @@ template <bool X32>
 __device__ __forceinline__ void few_load(const void* x, size_t at, float (&f)[8]) {
   if constexpr (X32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = p[0], b = p[1];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   } else {
-    few_unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at)), f);
+    few_unpack(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at), f);
   }
 }
 
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     for (int u = 0; u < U; ++u) {
       const int k = k0 + 256 * u;
       const bool in = k < p.K && rib_guard(w1 + k + 7, w_n, G_FEW_W);
-      a[u] = in ? __ldg(reinterpret_cast<const uint4*>(p.w + w0 + k)) : make_uint4(0, 0, 0, 0);
-      b[u] = in ? __ldg(reinterpret_cast<const uint4*>(p.w + w1 + k)) : make_uint4(0, 0, 0, 0);
+      a[u] = in ? *reinterpret_cast<const uint4*>(p.w + w0 + k) : make_uint4(0, 0, 0, 0);
+      b[u] = in ? *reinterpret_cast<const uint4*>(p.w + w1 + k) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -121,11 +121,11 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   if (lane >= (GATED ? R : 2 * R) || row >= p.rows || n >= p.N) return;
   const size_t at = static_cast<size_t>(row) * p.N + n;
   if (!rib_guard(at, static_cast<size_t>(p.rows) * p.N, G_FEW_OUT)) return;
-  const float z = mine + (p.bias ? __ldg(p.bias + n) : 0.f);
+  const float z = mine + (p.bias ? p.bias[n] : 0.f);
   float v, slope;
   act_both<ACT>(z, v, slope);
   if constexpr (GATED) {
-    static_cast<float*>(p.y)[at] = v * (other + (p.bias ? __ldg(p.bias + p.N + n) : 0.f));
+    static_cast<float*>(p.y)[at] = v * (other + (p.bias ? p.bias[p.N + n] : 0.f));
   } else {
     if (p.pre) p.pre[at] = __float2bfloat16_rn(z);
     if (p.residual) v += __bfloat162float(p.residual[at]);

@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             float4 bg = make_float4(0.f, 0.f, 0.f, 0.f), bu = bg;
             if (p.b_in && col < p.H &&
                 rib_guard(static_cast<size_t>(p.H) + col + 3, 2ull * p.H, G_GEMM_BIAS)) {
-              bg = __ldg(reinterpret_cast<const float4*>(p.b_in + col));
-              bu = __ldg(reinterpret_cast<const float4*>(p.b_in + p.H + col));
+              bg = *reinterpret_cast<const float4*>(p.b_in + col);
+              bu = *reinterpret_cast<const float4*>(p.b_in + p.H + col);
             }
             const float b4[4] = {bg.x, bg.y, bg.z, bg.w}, c4[4] = {bu.x, bu.y, bu.z, bu.w};
             float hv[4];

@@ -404,13 +404,13 @@ __device__ __forceinline__ void act_both(float z, float& a, float& da) {
 __device__ __forceinline__ void bias16(const float* bias, int col, int n, float4 (&b)[4]) {
   if (bias && col + 16 <= n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = __ldg(reinterpret_cast<const float4*>(bias + col) + e);
+    for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float4*>(bias + col)[e];
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       b[e] = bias && col + 4 * e < n &&
                      rib_guard(static_cast<size_t>(col) + 4 * e + 3, n, G_GEMM_BIAS)
-                 ? __ldg(reinterpret_cast<const float4*>(bias + col) + e)
+                 ? reinterpret_cast<const float4*>(bias + col)[e]
                  : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(256)
     for (int k = group * per; k < k1; ++k) {
       const size_t at = static_cast<size_t>(k) * n + at0;
       if (!rib_guard(at + 3, static_cast<size_t>(splits) * n, G_DW_RED)) continue;
-      const float4 v = __ldg(reinterpret_cast<const float4*>(src + at));
+      const float4 v = *reinterpret_cast<const float4*>(src + at);
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
   }
@@ -1154,8 +1154,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
       const long long r = r0 + k * step;
       const size_t at = static_cast<size_t>(r) * p.N + c;
       const bool ok = r < p.rows && rib_guard(at + 7, n, G_DZ_IN);
-      dv[k] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + at)) : make_uint4(0, 0, 0, 0);
-      zv[k] = ok && ACT != kActNone ? __ldg(reinterpret_cast<const uint4*>(p.pre + at))
+      dv[k] = ok ? *reinterpret_cast<const uint4*>(p.dy + at) : make_uint4(0, 0, 0, 0);
+      zv[k] = ok && ACT != kActNone ? *reinterpret_cast<const uint4*>(p.pre + at)
                                     : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll

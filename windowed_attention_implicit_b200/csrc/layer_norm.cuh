@@ -48,6 +48,9 @@ constexpr int G_LN_IN = 160, G_LN_OUT = 161, G_LN_STAT = 162, G_LN_PART = 163;
 // writes, before it touches global memory.  Only launch latency and a
 // kernel's set-up overlap the one before.  Every block of a kernel launched
 // this way calls it, so that kernels stay ordered one after the other.
+// What such a kernel reads may thus be written while it is already there: it
+// reads by plain loads behind the wait (and by TMA), never by the non-coherent
+// path, which takes data that is constant for the whole life of a kernel.
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 }
@@ -159,7 +162,7 @@ template <int V>
 __device__ __forceinline__ void ln_weight(const float* p, int c, bool in, float fill,
                                           float (&f)[V]) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = (p && in) ? __ldg(p + c + e) : fill;
+  for (int e = 0; e < V; ++e) f[e] = (p && in) ? p[c + e] : fill;
 }
 
 // Rows a group works on at once: as many as keep about 16 fp32 values of x
@@ -310,8 +313,8 @@ __global__ void __launch_bounds__(kLnThreads) ln_row_bwd_kernel(const LnParams p
         dr[k][i] = in ? L::load(p.dy, at) : L::zero();
         ar[k][i] = in && p.dres ? L::load(p.dres, at) : L::zero();
       }
-      mu[k] = row ? __ldg(p.mean + r0 + k) : 0.f;
-      rs[k] = row ? __ldg(p.rstd + r0 + k) : 0.f;
+      mu[k] = row ? p.mean[r0 + k] : 0.f;
+      rs[k] = row ? p.rstd[r0 + k] : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -574,8 +577,8 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
   }
   pdl_wait();
   for (int c = threadIdx.x; c < C; c += blockDim.x) {
-    s_gamma[ln_weight_slot<V>(c, C)] = p.gamma ? __ldg(p.gamma + c) : 1.f;
-    if (!BWD) s_beta[ln_weight_slot<V>(c, C)] = p.beta ? __ldg(p.beta + c) : 0.f;
+    s_gamma[ln_weight_slot<V>(c, C)] = p.gamma ? p.gamma[c] : 1.f;
+    if (!BWD) s_beta[ln_weight_slot<V>(c, C)] = p.beta ? p.beta[c] : 0.f;
   }
   __syncthreads();
   const float inv_c = 1.f / static_cast<float>(C);
@@ -626,8 +629,8 @@ __global__ void __launch_bounds__(BWD ? 384 : 512)
     if (BWD && b < blocks && lane < rows_of(b)) {
       const size_t r = static_cast<size_t>(b) * q.rows + lane;
       if (rib_guard(r, p.rows, G_LN_STAT)) {
-        mu_next = __ldg(p.mean + r);
-        rs_next = __ldg(p.rstd + r);
+        mu_next = p.mean[r];
+        rs_next = p.rstd[r];
       }
     }
   };
