@@ -136,3 +136,14 @@ def test_statistics_and_sums_that_nobody_wants_may_share_a_buffer():
     h = R.rib_layer_norm_bwd(x, dy, mean, rstd, dgamma=bin_[:96], dbeta=bin_[:96])
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(g["dx"], h["dx"])
+
+
+def test_a_feed_forward_workspace_for_a_few_more_rows_serves_fewer():
+    """Up to eight rows h is fp32, above bf16: the sizes still do not fall from
+    eight rows to nine (rows whose products run in one kernel need none)."""
+    for C, hidden in ((192, 384), (1024, 2816), (512, 8)):
+        sizes = [R.rib_gated_ffn_fwd_workspace(r, C, hidden) for r in range(1, 40)]
+        assert sizes == sorted(sizes) and sizes[7] >= 8 * hidden * 2
+    # what a call asks for is its own need
+    assert ffn_fwd(rows=9, ws=FAKE, wsb=9 * 192 * 2 - 1) == _abi.RIB_ERR_WORKSPACE
+    assert ffn_fwd(rows=9, ws=None) == _abi.RIB_ERR_WORKSPACE

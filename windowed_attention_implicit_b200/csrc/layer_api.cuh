@@ -659,6 +659,15 @@ bool fused_wins(int rows, int C, int hidden, int sms) {
   return C <= kFusedMaxC && (tiles >= sms / 2 || tiles >= 3 * div_up(hidden, 64));
 }
 
+// Bytes that the forward's h takes in HBM: fp32 for a few rows, bf16 between two
+// products, none in one kernel.
+size_t ffn_fwd_need(int rows, int C, int hidden) {
+  int sms = 0;
+  if (few_rows_win(rows, C, 2 * hidden)) return align256((size_t)rows * hidden * 4);
+  if (device_sms(&sms) == RIB_OK && fused_wins(rows, C, hidden, sms)) return 0;
+  return align256((size_t)rows * hidden * 2);
+}
+
 template <int ACT, bool RES>
 int launch_fused_as(const void* x, const void* w_in, const float* b_in, const void* w_out,
                     const float* b_out, const void* residual, void* y, int rows, int C, int H,
@@ -870,11 +879,13 @@ int rib_linear_bwd(const void* x, int rows, int K, const void* w, int N, int act
 }
 
 size_t rib_gated_ffn_fwd_workspace(int rows, int C, int hidden) {
-  int sms = 0;
   if (check_ffn(rows, C, hidden)) return 0;
-  if (few_rows_win(rows, C, 2 * hidden)) return align256((size_t)rows * hidden * 4);
-  if (device_sms(&sms) == RIB_OK && fused_wins(rows, C, hidden, sms)) return 0;
-  return align256((size_t)rows * hidden * 2);
+  size_t need = ffn_fwd_need(rows, C, hidden);
+  // at least what fewer rows need with h in fp32: a workspace for some rows serves
+  // the few that run without the tensor cores
+  for (int r = std::min(rows, kFewRows); need && r > 0; --r)
+    if (few_rows_win(r, C, 2 * hidden)) return std::max(need, align256((size_t)r * hidden * 4));
+  return need;
 }
 
 int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_in,
@@ -886,9 +897,7 @@ int rib_gated_ffn_fwd(const void* x, int rows, int C, int hidden, const void* w_
   if (rows == 0) return RIB_OK;
   if (!x || !w_in || !w_out || !y) return RIB_ERR_ARG;
   if (!aligned16_all({x, w_in, b_in, w_out, b_out, residual, y})) return RIB_ERR_ALIGN;
-  if ((rc = check_workspace(workspace, workspace_bytes,
-                            rib_gated_ffn_fwd_workspace(rows, C, hidden))))
-    return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes, ffn_fwd_need(rows, C, hidden)))) return rc;
   const size_t map = 2ull * rows * C, wts = 2ull * hidden * C, col = 4ull * hidden;
   if (clash_unless_same({y, map}, {{x, map}, {residual, map}})) return RIB_ERR_ARG;
   int sms = 0;
