@@ -20,6 +20,14 @@
 // column tile, mostly from L2: so the staging takes 16 columns at a time and a
 // fourth stage of x and dy fits beside the resident weights (119 -> 107 us; the
 // next kernel then meets more writes still on their way: 265 -> 262 in all).
+// The tensor core truncates when it adds to its accumulator, so g, u and dh drift
+// towards zero with the channels that are added up in one chain (dw_kernel), and
+// the bias gradients, fp32 sums of what is formed from them, with them: 2.1e-6 at
+// 1024 channels, a plain fp32 sum 0.4e-6.  Beyond kFfnChain k-steps the chains are
+// therefore cut (CHUNKED): each piece is a tile of its own to the MMA warp, and the
+// epilogue warps add the pieces to nearest, g and u in the tensor memory beside
+// the accumulators, dh in registers: 0.65e-6, for 4 % of the whole backward
+// (8192 rows of 1024, 2816 hidden: 406 -> 421 us).
 // Not kept: sixteen epilogue warps (124), tiles of 256 x 128 by CTA pairs, which
 // halve those reads but hold their accumulators longer (132).
 #pragma once
@@ -35,12 +43,15 @@ constexpr uint32_t kFfnB = 3u * 8192u;                    // Wg, Wu (K-major), W
 constexpr uint32_t kFfnOut = 32u * 32u;                   // a warp's staging: 32 rows x 16 columns
 constexpr uint32_t kFfnStaging = 8u * 3u * kFfnOut;
 constexpr int kFfnMaxStages = 6;
+constexpr int kFfnChain = 8;                              // k-steps (4 additions each) of one chain
+constexpr int kFfnPiece = 6;                              // at most, where chains are cut
 
 struct FfnBwdParams {
   const float* b_in;      // [2][H]; may be null
   float* part;            // [splits * 4][2][H] column sums of dg, du; null: not wanted
   int M, C, H;
   int m_tiles, n_tiles, splits, k_steps, stages, b_resident;
+  int piece;              // k-steps of a chain (CHUNKED)
   uint64_t wait_limit_ns;
 };
 
@@ -87,7 +98,7 @@ __device__ __forceinline__ void ffn_load_b(uint8_t* dst, const CUtensorMap* tm_i
 // 128; tm_in: w_in [2 H][C], boxes 64 x 64; tm_out: w_out [C][H], boxes 64 x
 // 64 (all 128-byte swizzle); tm_h: h [M][H], boxes 16 x 32, tm_d: dg | du
 // [M][2][H], boxes 16 x 1 x 32 (32-byte swizzle).
-template <int ACT>
+template <int ACT, bool CHUNKED>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x,
                    const __grid_constant__ CUtensorMap tm_dy,
@@ -104,6 +115,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   volatile int* ab = &bb.abort_flag;
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int items = p.n_tiles * p.splits;
+  const int piece = CHUNKED ? p.piece : p.k_steps;
   const uint64_t lim = p.wait_limit_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -180,33 +192,35 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     RingWait ring;
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x, ++n_item) {
       if (p.b_resident && !(ok = warp_wait(&bb.b_full, n_item & 1, ab, lim, SITE_FFN))) break;
-      for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits, ++t) {
-        const int a = t & 1;
-        if (t >= 2 && !(ok = warp_wait(&bb.acc_free[a], ((t >> 1) - 1) & 1, ab, lim, SITE_FFN)))
-          break;
-        for (int k = 0; k < p.k_steps; ++k) {
-          if (!(ok = ring.wait(&bb.full[st], ph, ab, lim, SITE_FFN))) break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(base + st * stage_bytes);
-          const uint32_t sb = p.b_resident ? smem_u32(s_res + k * kFfnB) : sa + kFfnA;
-          const uint64_t xd = make_sdesc(sa, 16, 1024, kLayoutSW128);
-          const uint64_t yd = make_sdesc(sa + kGemmATile, 16, 1024, kLayoutSW128);
-          const uint64_t wd = make_sdesc(sb, 16, 1024, kLayoutSW128);
-          const uint64_t od = make_sdesc(sb + 16384, 8192, 1024, kLayoutSW128);
-          const int steps = k + 1 == p.k_steps ? last_steps : 4;
-          uint64_t* done = &bb.empty[st];
-          if (++st == p.stages) {
-            st = 0;
-            ph ^= 1;
+      for (int m = it / p.n_tiles; ok && m < p.m_tiles; m += p.splits)
+        for (int k0 = 0; ok && k0 < p.k_steps; k0 += piece, ++t) {   // t: chains so far
+          const int a = t & 1;
+          if (t >= 2 && !(ok = warp_wait(&bb.acc_free[a], ((t >> 1) - 1) & 1, ab, lim, SITE_FFN)))
+            break;
+          const int k1 = min(k0 + piece, p.k_steps);
+          for (int k = k0; k < k1; ++k) {
+            if (!(ok = ring.wait(&bb.full[st], ph, ab, lim, SITE_FFN))) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(base + st * stage_bytes);
+            const uint32_t sb = p.b_resident ? smem_u32(s_res + k * kFfnB) : sa + kFfnA;
+            const uint64_t xd = make_sdesc(sa, 16, 1024, kLayoutSW128);
+            const uint64_t yd = make_sdesc(sa + kGemmATile, 16, 1024, kLayoutSW128);
+            const uint64_t wd = make_sdesc(sb, 16, 1024, kLayoutSW128);
+            const uint64_t od = make_sdesc(sb + 16384, 8192, 1024, kLayoutSW128);
+            const int steps = k + 1 == p.k_steps ? last_steps : 4;
+            uint64_t* done = &bb.empty[st];
+            if (++st == p.stages) {
+              st = 0;
+              ph ^= 1;
+            }
+            ring.peek(&bb.full[st], ph);
+            const uint32_t acc = k > k0 ? 1u : 0u;
+            pair_umma_steps<1>(steps, tmem + 256 * a, xd, 2, wd, 2, id_gu, acc);
+            pair_umma_steps<1>(steps, tmem + 256 * a + 128, yd, 2, od, 128, id_dh, acc);
+            umma_commit_elect(done);
           }
-          ring.peek(&bb.full[st], ph);
-          const uint32_t acc = k > 0 ? 1u : 0u;
-          pair_umma_steps<1>(steps, tmem + 256 * a, xd, 2, wd, 2, id_gu, acc);
-          pair_umma_steps<1>(steps, tmem + 256 * a + 128, yd, 2, od, 128, id_dh, acc);
-          umma_commit_elect(done);
+          if (ok) umma_commit_elect(&bb.acc_full[a]);
         }
-        if (ok) umma_commit_elect(&bb.acc_full[a]);
-      }
       if (ok && p.b_resident) umma_commit_elect(&bb.b_free);
     }
     umma_commit_elect(&bb.drain);
@@ -226,6 +240,56 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       const int split = it / p.n_tiles;
       float sum_g[2] = {0.f, 0.f}, sum_u[2] = {0.f, 0.f};
       for (int m = split; m < p.m_tiles; m += p.splits, ++t) {
+        // the pieces before a tile's last one: added up, g and u in the columns
+        // behind the accumulators (which only this warp touches)
+        [[maybe_unused]] float dh[CHUNKED ? 32 : 1];
+        const uint32_t sum_gu = tmem + 192 + lane_off + 32 * half;   // g; u 256 columns on
+        if constexpr (CHUNKED) {
+          for (int k1 = piece; k1 < p.k_steps; k1 += piece, ++t) {
+            const int b = t & 1;
+            if (!(ok = warp_wait(&bb.acc_full[b], (t >> 1) & 1, ab, lim, SITE_FFN))) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + 256 * b + lane_off + 32 * half;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t g[16], u[16], d[16];
+              tmem_ld_x16(acc + 16 * h, g);
+              tmem_ld_x16(acc + 64 + 16 * h, u);
+              tmem_ld_x16(acc + 128 + 16 * h, d);
+              if (k1 > piece) {
+                uint32_t sg[16], su[16];
+                tmem_ld_x16(sum_gu + 16 * h, sg);
+                tmem_ld_x16(sum_gu + 256 + 16 * h, su);
+                tmem_wait_ld();
+                reg_fence_x16(g);
+                reg_fence_x16(u);
+                reg_fence_x16(d);
+                reg_fence_x16(sg);
+                reg_fence_x16(su);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  g[e] = __float_as_uint(__uint_as_float(g[e]) + __uint_as_float(sg[e]));
+                  u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(su[e]));
+                  dh[16 * h + e] += __uint_as_float(d[e]);
+                }
+              } else {
+                tmem_wait_ld();
+                reg_fence_x16(g);
+                reg_fence_x16(u);
+                reg_fence_x16(d);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) dh[16 * h + e] = __uint_as_float(d[e]);
+              }
+              tmem_st_x16(sum_gu + 16 * h, g);
+              tmem_st_x16(sum_gu + 256 + 16 * h, u);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bb.acc_free[b]);
+          }
+          if (!ok) break;
+        }
         const int a = t & 1;
         const int row0 = 128 * m + 32 * quarter;
         if (!(ok = warp_wait(&bb.acc_full[a], (t >> 1) & 1, ab, lim, SITE_FFN))) break;
@@ -237,10 +301,28 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           tmem_ld_x16(acc + 16 * h, g);
           tmem_ld_x16(acc + 64 + 16 * h, u);
           tmem_ld_x16(acc + 128 + 16 * h, d);
-          tmem_wait_ld();
-          reg_fence_x16(g);
-          reg_fence_x16(u);
-          reg_fence_x16(d);
+          if constexpr (CHUNKED) {
+            uint32_t pg[16], pu[16];
+            tmem_ld_x16(sum_gu + 16 * h, pg);
+            tmem_ld_x16(sum_gu + 256 + 16 * h, pu);
+            tmem_wait_ld();
+            reg_fence_x16(g);
+            reg_fence_x16(u);
+            reg_fence_x16(d);
+            reg_fence_x16(pg);
+            reg_fence_x16(pu);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              g[e] = __float_as_uint(__uint_as_float(g[e]) + __uint_as_float(pg[e]));
+              u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(pu[e]));
+              d[e] = __float_as_uint(__uint_as_float(d[e]) + dh[16 * h + e]);
+            }
+          } else {
+            tmem_wait_ld();
+            reg_fence_x16(g);
+            reg_fence_x16(u);
+            reg_fence_x16(d);
+          }
           if (h == 1) {   // the accumulators are in registers
             tc_fence_before();
             __syncwarp();

@@ -619,8 +619,8 @@ int launch_dz(const DzParams& p, int row_splits, cudaStream_t st) {
   return launch(dz_kernel<ACT>, dim3(div_up(p.N, 256), row_splits), 256, 0, st, 1, p);
 }
 
-template <int ACT>
-int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void* w_in,
+template <int ACT, bool CHUNKED>
+int launch_ffn_bwd_as(const FfnBwdWs& w, const void* x, const void* dy, const void* w_in,
                    const void* w_out, const FfnBwdParams& p, uint8_t* ws, cudaStream_t st) {
   CUtensorMap tx, ty, ti, to, th, td;
   int rc = map_2d(&tx, x, p.M, p.C, 64, 128);
@@ -636,10 +636,18 @@ int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void*
                   CU_TENSOR_MAP_SWIZZLE_32B);
   }
   if (rc) return rc;
-  if ((rc = set_smem(ffn_bwd_kernel<ACT>, w.f.smem))) return rc;
+  if ((rc = set_smem(ffn_bwd_kernel<ACT, CHUNKED>, w.f.smem))) return rc;
   TraceScope ts(K_FFN_BWD, st);
-  return launch(ffn_bwd_kernel<ACT>, dim3(w.f.grid), kFfnThreads, w.f.smem, st, 1, tx, ty, ti, to,
+  return launch(ffn_bwd_kernel<ACT, CHUNKED>, dim3(w.f.grid), kFfnThreads, w.f.smem, st, 1, tx, ty, ti, to,
                 th, td, p);
+}
+
+template <int ACT>
+int launch_ffn_bwd(const FfnBwdWs& w, const void* x, const void* dy, const void* w_in,
+                   const void* w_out, FfnBwdParams p, uint8_t* ws, cudaStream_t st) {
+  if (p.k_steps <= kFfnChain) return launch_ffn_bwd_as<ACT, false>(w, x, dy, w_in, w_out, p, ws, st);
+  p.piece = div_up(p.k_steps, div_up(p.k_steps, kFfnPiece));   // pieces of about the same length
+  return launch_ffn_bwd_as<ACT, true>(w, x, dy, w_in, w_out, p, ws, st);
 }
 
 // ---------------------------------------------------------------- fused feed-forward
